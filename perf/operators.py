@@ -190,7 +190,9 @@ def prepare(c, seed):
 
     held, page = lens(c), c["page"]
     T = c.get("T", 0)
-    per = [(max(0, n) + T + page - 1) // page for n in held]
+    # a bounded row grows to its budget over the passes, whatever it holds before the first
+    most = [c["budget"] if c["kind"] in ("evict", "step") else max(0, n) for n in held]
+    per = [(n + T + page - 1) // page for n in most]
     width, pool = max(1, max(per)), sum(per) + 3
     order = torch.randperm(pool, generator=gen, device=dev).tolist()
     table = torch.full((B, width), -1, dtype=torch.int32)
