@@ -382,6 +382,183 @@ TC_API tc_status tc_decode_step_host(tc_decode_state *state, const void *q_t, co
                               const void *v_t, void *y_t, void *workspace,
                               size_t workspace_bytes, tc_stream_t stream);
 
+/* ---- Rotary positions -----------------------------------------------------
+ * The layer's queries and keys carry their positions as rotations, applied
+ * before the keys enter the window (§3.1).  A head's leading `rot` dimensions
+ * are pairs; pair i of the token at position p is turned by the angle p f'_i,
+ *   f_i = base^(-2i/rot),  i < rot/2,
+ *   f'_i = f_i (s_i + (1 - s_i)/factor),
+ *   s_i = clamp((train_len f_i / 2 pi - low) / (high - low), 0, 1)
+ *         (0 for every i when high <= low),
+ * and scaled by `gain`:
+ *   (x, z) -> gain (x cos a - z sin a, x sin a + z cos a).
+ * factor = 1 is the plain rotation; factor > 1 with high <= low divides every
+ * position by factor (linear interpolation); with 0 <= low < high the pairs
+ * that turn more than `high` times over train_len tokens keep their frequency,
+ * those that turn less than `low` times are slowed by factor, and the ones
+ * between are blended (interpolation by parts, Peng et al. 2023).  The angle
+ * is formed from the position in 64-bit fixed point, as a fraction of a turn,
+ * so far positions lose nothing. */
+typedef struct tc_rotary {
+    int64_t rot;       /* rotated leading dimensions: even, 0 <= rot <= d <= 128 */
+    int64_t interleaved; /* 0: pair i = (i, i + rot/2); 1: pair i = (2i, 2i + 1) */
+    double base;       /* > 1                                                  */
+    double factor;     /* >= 1                                                 */
+    double low, high;  /* turns over train_len; high <= low: no ramp           */
+    double train_len;  /* >= 0, used by the ramp only                          */
+    double gain;       /* finite; multiplies the rotated part                  */
+} tc_rotary;
+
+#define TC_ROTATE_BACKWARD 1u /* the transposed rotation: gradients of the inputs
+                                 from gradients of the outputs                */
+
+/* Shapes of one tc_rotate call.  q [B,Hq,T,d] and k [B,H,T,d] (H = 0: no k),
+ * the head dimension contiguous; strides in elements of dimensions b, h, t.
+ * Inputs may have stride 0 (broadcast); outputs must not overlap themselves:
+ * their strides, sorted, must nest (each at least the extent below it).
+ * 0 <= B, T; 1 <= Hq; 0 <= H; 1 <= d <= 128; B T (Hq + H) d <= 2^38. */
+typedef struct tc_rotate_desc {
+    int64_t B, Hq, H, T, d;
+    tc_dtype dtype;  /* of q, k and the outputs                               */
+    uint32_t flags;  /* TC_ROTATE_* bits                                      */
+    int64_t q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];
+} tc_rotate_desc;
+
+/* Turns q and k (one launch) by their positions: token t of row b is at
+ * positions[b*T + t] (int64 device [B,T], 8-byte aligned) or, with positions
+ * NULL, at t0 + t.  Dimensions rot .. d-1 are copied.  float32 arithmetic, one
+ * rounding to dtype.  An output may be its input with the same strides (in
+ * place); otherwise the address ranges of an input and its output must not
+ * meet (TC_ERR_INVALID_ARG), and q's rows and k's must not overlap the other's
+ * output.  q, k and the outputs
+ * need the alignment of their type only (16-byte alignment of addresses and
+ * strides, and d and rot/2 in whole 16-byte vectors, run the faster kernel).
+ * For training, the gradients tc_backward returns (float32) go through the
+ * same call with TC_ROTATE_BACKWARD.  Errors: TC_ERR_INVALID_ARG,
+ * TC_ERR_UNSUPPORTED, TC_ERR_NO_DEVICE, TC_ERR_CUDA. */
+TC_API tc_status tc_rotate(const tc_rotate_desc *desc, const tc_rotary *rotary,
+                           const int64_t *positions, int64_t t0, const void *q, const void *k,
+                           void *q_out, void *k_out, tc_stream_t stream);
+
+/* ---- Paged cache that forgets its least attended pairs -----------------------
+ * The streaming state of one layer for rows of different lengths and grouped
+ * heads: where tc_decode_state's ring drops the oldest pair, this cache drops
+ * the pair that the queries have attended to least, and writes it into the
+ * memory A by the layer's own rule (Fig. 2 step (3)).  With every weight equal
+ * the oldest pair leaves first, which is the layer's sliding window.
+ *
+ * Row b holds len[b] pairs in slots 0 .. len[b]-1; slot s lives in page
+ * table[b][s / page], at row s mod page of that page, the same for every head.
+ * Slots carry no order: a pair's position is in pos (and, rotated, in its key).
+ * All arrays are caller-owned device memory, updated in place.  Rows must not
+ * share pages, except that rows which are only attended to without
+ * TC_CACHE_ACCUMULATE may share any.
+ *   1 <= B <= 65535; 1 <= H; B H <= 2^20; d in {16, 32, 64, 128} (d_k = d_v);
+ *   page a multiple of 16, at most 4096; 1 <= max_pages;
+ *   n_pages H page < 2^31; max_pages page <= 2^24; B max_pages page <= 2^36.
+ * The table, len, clock and counts are device data, which the host cannot
+ * check: the kernels do.  A row whose len exceeds max_pages*page is skipped;
+ * tc_cache_append, tc_cache_evict and tc_cache_step skip a row that has an
+ * entry outside 0 .. n_pages-1 among the pages they need; tc_cache_attend
+ * leaves such a page's pairs out.  Each sets TC_ERR_DEVICE_BOUNDS in the device
+ * status word; nothing outside the buffers is read or written. */
+typedef struct tc_paged_cache {
+    int64_t B, H, d;             /* rows, key/value heads, head dimension      */
+    int64_t page, n_pages, max_pages; /* slots a page, pages in the pool, table width */
+    tc_dtype dtype;              /* of k_pages, v_pages and the call's q, k, v, y */
+    void *k_pages, *v_pages;     /* [n_pages,H,page,d]                         */
+    float *mass;                 /* [n_pages,H,page] accumulated weight; NULL when no
+                                    call accumulates or evicts                 */
+    int32_t *pos;                /* [n_pages,H,page] position of the pair; NULL as mass */
+    const int32_t *table;        /* [B,max_pages]; entries past a row's pages are not read */
+    int64_t *len;                /* [B] pairs held; negative: an empty row, which every
+                                    call leaves untouched                      */
+    int64_t *clock;              /* [B] tokens consumed: the next token's position */
+    float *A;                    /* [B,H,d,d], the memory; NULL: none          */
+    const float *lambda, *eta;   /* [H]; NULL when A is                        */
+} tc_paged_cache;
+
+#define TC_CACHE_ACCUMULATE 1u /* add each pair's attention weight to mass */
+
+/* Appends tokens: token i < counts[b] (counts NULL: T for every row) of row b
+ * goes to slot len[b] + i with position clock[b] + i; its key is rotated by
+ * that position (rotary NULL: stored as it is), mass becomes mass_in (NULL: 0)
+ * and pos the position.  q (NULL allowed), the same tokens' queries, is rotated
+ * into q_out.  Then clock[b] and len[b] grow by counts[b].  A row is skipped
+ * with TC_ERR_DEVICE_BOUNDS when the tokens do not fit its table, counts[b] is
+ * negative or above T, or a position would pass 2^31 - 1.
+ *   k, v [B,H,T,d], q [B,Hq,T,d]: strides in elements of b, h, t in kv_stride
+ *   (k), v_stride, q_stride; the head dimension contiguous.
+ *   q_out [B,Hq,T,d] contiguous; rows past counts[b] are not written.
+ *   mass_in [B,H,T] float32, counts [B] int64, both device.
+ * cache->mass and pos may be NULL (a cache that never evicts).
+ * Errors as tc_rotate. */
+typedef struct tc_append_args {
+    int64_t T, Hq;
+    const void *q, *k, *v;
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+    const int64_t *counts;
+    const float *mass_in;
+    void *q_out;
+} tc_append_args;
+TC_API tc_status tc_cache_append(const tc_paged_cache *cache, const tc_rotary *rotary,
+                                 const tc_append_args *args, tc_stream_t stream);
+
+/* Attention of one new token per row over the row's pairs, fused with the
+ * memory's read (Fig. 2 step (5)): for query head h, which reads key/value head
+ * h / (Hq/H),
+ *   p = softmax_j(<q,k_j>/sqrt(d)),  y = sum_j p_j v_j + sigmoid(g_h) q A.
+ * A row that holds no pair gives the memory's read alone.  With
+ * TC_CACHE_ACCUMULATE mass_j grows by the sum of p_j over the heads that share
+ * the key/value head.
+ *   q, y [B,Hq,d] contiguous, Hq a multiple of H, Hq/H <= 128; g [Hq] float32, NULL exactly
+ *   when cache->A is NULL or the memory is not to be read.
+ * Work is split over the lengths and joined: two launches.  Every sum has a
+ * fixed order on a given device.  Workspace:
+ * tc_cache_attend_workspace_size(cache, Hq, flags) bytes ((size_t)-1 when
+ * invalid).  Errors as tc_prefill. */
+TC_API size_t tc_cache_attend_workspace_size(const tc_paged_cache *cache, int64_t Hq, uint32_t flags);
+TC_API tc_status tc_cache_attend(const tc_paged_cache *cache, int64_t Hq, const void *q, const float *g,
+                                 void *y, uint32_t flags, void *workspace, size_t workspace_bytes,
+                                 tc_stream_t stream);
+
+/* Evicts each row's least attended pairs until it holds at most `budget`, per
+ * head: while more are held, the pair with the smallest (protected, mass, pos)
+ * leaves, where protected = pos >= clock - recent; NaN counts as the largest
+ * mass, equal pairs go by slot.  Every pair that leaves is written,
+ * A <- lambda A + eta k v^T, in the order of leaving (A is computed from the
+ * weighted sums, as tc_prefill's chunk scan does; skipped when A is NULL).  Then
+ * the pairs left in slots >= budget move, in ascending order, to the freed
+ * slots below budget, in ascending order, and len becomes budget.
+ *   budget >= 1; 0 <= recent; cache->mass and pos are required.
+ * Workspace: tc_cache_evict_workspace_size(cache) bytes.  Errors as
+ * tc_prefill. */
+TC_API size_t tc_cache_evict_workspace_size(const tc_paged_cache *cache);
+TC_API tc_status tc_cache_evict(const tc_paged_cache *cache, int64_t budget, int64_t recent,
+                                void *workspace, size_t workspace_bytes, tc_stream_t stream);
+
+/* One serving step for every row, in the order of Fig. 2: tc_cache_append of
+ * one token, tc_cache_evict down to budget, tc_cache_attend with the token's
+ * query; the same results in three launches.
+ *   q [B,Hq,d], k, v [B,H,d]: not rotated (rotary NULL: used as they are);
+ *   strides in elements of b and h (slices of a fused projection), the head
+ *   dimension contiguous, the alignment of their type; y [B,Hq,d] contiguous.
+ *   g, budget, recent, flags as in the three calls; mass and pos are required.
+ * Workspace: tc_cache_step_workspace_size(cache, Hq, flags) bytes. */
+typedef struct tc_step_args {
+    int64_t Hq;
+    const void *q, *k, *v;
+    int64_t q_stride[2], k_stride[2], v_stride[2];
+    const float *g;
+    void *y;
+    int64_t budget, recent;
+    uint32_t flags; /* TC_CACHE_* bits */
+} tc_step_args;
+TC_API size_t tc_cache_step_workspace_size(const tc_paged_cache *cache, int64_t Hq, uint32_t flags);
+TC_API tc_status tc_cache_step(const tc_paged_cache *cache, const tc_rotary *rotary,
+                               const tc_step_args *args, void *workspace, size_t workspace_bytes,
+                               tc_stream_t stream);
+
 /* Limit, in nanoseconds, of every bounded wait inside the tensor-core prefill
  * kernels (an mbarrier wait for a copy, a tensor-core product or another warp).
  * A wait that runs out makes the kernel drain its copies and products, record

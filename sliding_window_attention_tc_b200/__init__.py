@@ -53,7 +53,11 @@ EXPORTED = ("tc_prefill_workspace_size", "tc_prefill", "tc_prefill_launch_count"
             "tc_state_fold", "tc_decode_step_ragged", "tc_backward", "tc_backward_workspace_size",
             "tc_set_wait_limit_ns", "tc_prefill_varlen", "tc_prefill_varlen_workspace_size",
             "tc_backward_launch_count", "tc_set_prefill_path", "tc_get_prefill_path",
-            "tc_prefill_path_for")
+            "tc_prefill_path_for", "tc_rotate", "tc_cache_append", "tc_cache_attend",
+            "tc_cache_attend_workspace_size", "tc_cache_evict", "tc_cache_evict_workspace_size",
+            "tc_cache_step", "tc_cache_step_workspace_size")
+TC_ROTATE_BACKWARD = 1
+TC_CACHE_ACCUMULATE = 1
 
 
 class PrefillDesc(ctypes.Structure):
@@ -69,6 +73,48 @@ class DecodeStateC(ctypes.Structure):
                 ("ring_v", ctypes.c_void_p), ("A", ctypes.c_void_p),
                 ("lam", ctypes.c_void_p), ("eta", ctypes.c_void_p), ("g", ctypes.c_void_p),
                 ("write_rule", ctypes.c_int)]
+
+
+class RotaryC(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int64), ("interleaved", ctypes.c_int64), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("train_len", ctypes.c_double), ("gain", ctypes.c_double)]
+
+
+_I3 = ctypes.c_int64 * 3
+
+
+class RotateDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("Hq", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("T", ctypes.c_int64), ("d", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("flags", ctypes.c_uint32), ("q_stride", _I3), ("k_stride", _I3),
+                ("q_out_stride", _I3), ("k_out_stride", _I3)]
+
+
+class PagedCacheC(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("H", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("page", ctypes.c_int64), ("n_pages", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("mass", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("len", ctypes.c_void_p), ("clock", ctypes.c_void_p), ("A", ctypes.c_void_p),
+                ("lam", ctypes.c_void_p), ("eta", ctypes.c_void_p)]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("Hq", ctypes.c_int64), ("q", ctypes.c_void_p),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_stride", _I3),
+                ("k_stride", _I3), ("v_stride", _I3), ("counts", ctypes.c_void_p),
+                ("mass_in", ctypes.c_void_p), ("q_out", ctypes.c_void_p)]
+
+
+_I2 = ctypes.c_int64 * 2
+
+
+class StepArgs(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int64), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("q_stride", _I2), ("k_stride", _I2), ("v_stride", _I2),
+                ("g", ctypes.c_void_p), ("y", ctypes.c_void_p), ("budget", ctypes.c_int64),
+                ("recent", ctypes.c_int64), ("flags", ctypes.c_uint32)]
 
 
 _vp, _sz, _int = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
@@ -124,6 +170,24 @@ _lib.tc_get_prefill_path.argtypes = []
 _lib.tc_get_prefill_path.restype = _int
 _lib.tc_prefill_path_for.argtypes = [_PD, ctypes.c_int64]
 _lib.tc_prefill_path_for.restype = _int
+
+_PC, _PR = ctypes.POINTER(PagedCacheC), ctypes.POINTER(RotaryC)
+_lib.tc_rotate.argtypes = [ctypes.POINTER(RotateDesc), _PR, _vp, ctypes.c_int64] + [_vp] * 4 + [_vp]
+_lib.tc_rotate.restype = _int
+_lib.tc_cache_append.argtypes = [_PC, _PR, ctypes.POINTER(AppendArgs), _vp]
+_lib.tc_cache_append.restype = _int
+_lib.tc_cache_attend_workspace_size.argtypes = [_PC, ctypes.c_int64, ctypes.c_uint32]
+_lib.tc_cache_attend_workspace_size.restype = _sz
+_lib.tc_cache_attend.argtypes = [_PC, ctypes.c_int64, _vp, _vp, _vp, ctypes.c_uint32, _vp, _sz, _vp]
+_lib.tc_cache_attend.restype = _int
+_lib.tc_cache_evict_workspace_size.argtypes = [_PC]
+_lib.tc_cache_evict_workspace_size.restype = _sz
+_lib.tc_cache_evict.argtypes = [_PC, ctypes.c_int64, ctypes.c_int64, _vp, _sz, _vp]
+_lib.tc_cache_evict.restype = _int
+_lib.tc_cache_step_workspace_size.argtypes = [_PC, ctypes.c_int64, ctypes.c_uint32]
+_lib.tc_cache_step_workspace_size.restype = _sz
+_lib.tc_cache_step.argtypes = [_PC, _PR, ctypes.POINTER(StepArgs), _vp, _sz, _vp]
+_lib.tc_cache_step.restype = _int
 
 SIZE_ERROR = ctypes.c_size_t(-1).value
 
@@ -644,6 +708,327 @@ def decode_step_host(state: DecodeState, q, k, v, y, *, workspace, stream=None):
                                   _stream(stream))
     _check(st, "tc_decode_step_host")
     state.t = int(cs.t)
+    return y
+
+
+# ---- rotary positions and the paged cache --------------------------------------
+
+class Rotary:
+    """Rotary positions (tc_rotary): the head's leading `rot` dimensions are
+    turned by position * frequency.  `interleaved` pairs neighbours instead of
+    halves; factor, low, high and train_len extend the context (factor alone:
+    linear interpolation; with low < high: by parts); gain multiplies the
+    rotated part.  Immutable; make it once and pass it to every call."""
+
+    __slots__ = ("c", "ref")
+
+    def __init__(self, rot: int, base: float = 10000.0, *, interleaved: bool = False,
+                 factor: float = 1.0, low: float = 0.0, high: float = 0.0, train_len: float = 0.0,
+                 gain: float = 1.0):
+        if rot < 0 or rot % 2:
+            raise ValueError("rot must be even and not negative")
+        object.__setattr__(self, "c", RotaryC(int(rot), int(bool(interleaved)), float(base),
+                                              float(factor), float(low), float(high),
+                                              float(train_len), float(gain)))
+        object.__setattr__(self, "ref", ctypes.pointer(self.c))
+
+    def __setattr__(self, name, value):
+        raise AttributeError("Rotary is immutable")
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _rows(t: Optional[torch.Tensor], name: str, shape, dtype):
+    """[b,h,t,d] rows with a contiguous head dimension; returns the strides."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}; expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
+    s = t.stride()
+    if s[3] != 1 and shape[3] > 1:
+        raise ValueError(f"{name}: the head dimension must be contiguous")
+    return s[:3]
+
+
+def _token_rows(t: torch.Tensor, name: str, shape, dtype):
+    """[b,h,d] rows with a contiguous head dimension; returns the strides."""
+    _expect(t, name, shape, dtype)
+    s = t.stride()
+    if s[2] != 1 and shape[2] > 1:
+        raise ValueError(f"{name}: the head dimension must be contiguous")
+    return s[:2]
+
+
+def _rotate(q, k, rotary, positions, t0, q_out, k_out, flags, stream):
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q and k must be [B,heads,T,d]")
+    B, Hq, T, d = q.shape
+    dt = _dtype_code(q)
+    H = 0 if k is None else k.shape[1]
+    if q_out is None:
+        q_out = torch.empty((B, Hq, T, d), dtype=q.dtype, device=q.device)
+    qs, qos = _rows(q, "q", q.shape, q.dtype), _rows(q_out, "q_out", q.shape, q.dtype)
+    ks = kos = (0, 0, 0)
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty((B, H, T, d), dtype=q.dtype, device=q.device)
+        ks, kos = _rows(k, "k", (B, H, T, d), q.dtype), _rows(k_out, "k_out", (B, H, T, d), q.dtype)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if positions is not None:
+        _expect(positions, "positions", (B, T), torch.int64)
+        _contig(positions)
+    _dev_check(q, k, q_out, k_out, positions)
+    desc = RotateDesc(B, Hq, H, T, d, dt, flags, _I3(*qs), _I3(*ks), _I3(*qos), _I3(*kos))
+    _check(_lib.tc_rotate(ctypes.byref(desc), rotary.ref, None if positions is None else positions.data_ptr(),
+                          int(t0), q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+                          None if k is None else k_out.data_ptr(), _raw_stream(stream)), "tc_rotate")
+    return q_out, k_out
+
+
+def rotate(q: torch.Tensor, k: Optional[torch.Tensor], rotary: Rotary, *,
+           positions: Optional[torch.Tensor] = None, t0: int = 0, q_out: Optional[torch.Tensor] = None,
+           k_out: Optional[torch.Tensor] = None, stream=None):
+    """tc_rotate: q [B,Hq,T,d] and k [B,H,T,d] (or None) turned by their
+    positions: positions [B,T] int64, or t0, t0 + 1, ...  Any strides with a
+    contiguous head dimension (slices of a fused projection, transposed
+    views); the outputs are contiguous [B,heads,T,d] unless given, and may be
+    the inputs.  Returns (q_out, k_out)."""
+    return _rotate(q, k, rotary, positions, t0, q_out, k_out, 0, stream)
+
+
+def rotate_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], rotary: Rotary, *,
+                    positions: Optional[torch.Tensor] = None, t0: int = 0,
+                    dq_out: Optional[torch.Tensor] = None, dk_out: Optional[torch.Tensor] = None,
+                    stream=None):
+    """tc_rotate with TC_ROTATE_BACKWARD: gradients of rotate's inputs from
+    gradients of its outputs (those that backward returns, for instance)."""
+    return _rotate(dq, dk, rotary, positions, t0, dq_out, dk_out, TC_ROTATE_BACKWARD, stream)
+
+
+class PagedCache:
+    """Paged streaming state (tc_paged_cache): caller-owned device tensors,
+    updated in place by the cache_* calls.
+
+    k_pages, v_pages [n_pages,H,page,d] (float32 or bfloat16), table
+    [B,max_pages] int32, lens and clocks [B] int64 (pairs held; tokens consumed;
+    a negative length is an empty row); mass float32 and pos int32
+    [n_pages,H,page] for accumulation and eviction; A [B,H,d,d] float32 with
+    lam, eta [H] for the memory.  The tensors are checked here, once, and
+    cannot be exchanged afterwards (their contents can)."""
+
+    __slots__ = ("k_pages", "v_pages", "table", "lens", "clocks", "mass", "pos", "A", "lam", "eta",
+                 "c", "ref", "B", "H", "d", "dtype", "device")
+
+    def __init__(self, k_pages, v_pages, table, lens, clocks, *, mass=None, pos=None, A=None, lam=None,
+                 eta=None):
+        if k_pages.dim() != 4 or table.dim() != 2:
+            raise ValueError("k_pages must be [n_pages,H,page,d] and table [B,max_pages]")
+        n_pages, H, page, d = k_pages.shape
+        B, max_pages = table.shape
+        dt = _dtype_code(k_pages)
+        _expect(v_pages, "v_pages", k_pages.shape, k_pages.dtype)
+        _expect(table, "table", (B, max_pages), torch.int32)
+        _expect(lens, "lens", (B,), torch.int64)
+        _expect(clocks, "clocks", (B,), torch.int64)
+        _expect(mass, "mass", (n_pages, H, page), torch.float32)
+        _expect(pos, "pos", (n_pages, H, page), torch.int32)
+        if (mass is None) != (pos is None):
+            raise ValueError("mass and pos go together")
+        _expect(A, "A", (B, H, d, d), torch.float32)
+        if A is not None:
+            if lam is None or eta is None:
+                raise ValueError("A needs lam and eta")
+            _expect(lam, "lam", (H,), torch.float32)
+            _expect(eta, "eta", (H,), torch.float32)
+        ts = (k_pages, v_pages, table, lens, clocks, mass, pos, A, lam, eta)
+        _contig(*ts)
+        if any(t is not None and t.device != k_pages.device for t in ts):
+            raise ValueError("the cache's tensors must be on one device")
+        p = [None if t is None else t.data_ptr() for t in ts]
+        c = PagedCacheC(B, H, d, page, n_pages, max_pages, dt, p[0], p[1], p[5], p[6], p[2], p[3], p[4],
+                        p[7], p[8] if A is not None else None, p[9] if A is not None else None)
+        for name, x in zip(self.__slots__, ts + (c, ctypes.pointer(c), B, H, d, k_pages.dtype, k_pages.device)):
+            object.__setattr__(self, name, x)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a PagedCache's tensors are fixed; make another one")
+
+    @staticmethod
+    def empty(B, H, d, page, n_pages, max_pages, *, lam=None, eta=None, dtype=torch.bfloat16,
+              device="cuda"):
+        """An empty cache: rows hold nothing (lens 0), no page is dealt (table
+        -1: the caller's allocator fills it), with a memory when lam and eta
+        are given."""
+        f = dict(dtype=torch.float32, device=device)
+        return PagedCache(torch.zeros((n_pages, H, page, d), dtype=dtype, device=device),
+                          torch.zeros((n_pages, H, page, d), dtype=dtype, device=device),
+                          torch.full((B, max_pages), -1, dtype=torch.int32, device=device),
+                          torch.zeros(B, dtype=torch.int64, device=device),
+                          torch.zeros(B, dtype=torch.int64, device=device),
+                          mass=torch.zeros((n_pages, H, page), **f),
+                          pos=torch.zeros((n_pages, H, page), dtype=torch.int32, device=device),
+                          A=None if lam is None else torch.zeros((B, H, d, d), **f), lam=lam, eta=eta)
+
+    def here(self, *ts):
+        """The other tensors of a call are where the cache is, and that is the
+        current device."""
+        dev = self.device
+        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+            raise ValueError(f"the cache is on {dev} but the current CUDA device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        for t in ts:
+            if t is not None and t.device != dev:
+                raise ValueError(f"tensor on {t.device}; the cache is on {dev}")
+
+
+def _workspace(size: int, where: str, workspace, device):
+    if size == SIZE_ERROR:
+        raise TCError(1, where)
+    if workspace is None:
+        workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=device)
+    elif not workspace.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _new_workspace(size: int, where: str, cache):
+    return _workspace(size, where, None, cache.device)[0]
+
+
+def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, rotary: Optional[Rotary] = None,
+                 q: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                 mass: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, stream=None):
+    """tc_cache_append: tokens k, v [B,H,T,d] enter their rows' pages, k rotated
+    by the row's clock (rotary None: as it is); of row b the first counts[b]
+    (int64 [B]; None: all T).  mass [B,H,T] float32: the weights they start
+    with (None: 0).  q [B,Hq,T,d], the same tokens' queries, is rotated into
+    q_out, which is returned (None without q).  k, v and q may have any strides
+    with a contiguous head dimension."""
+    if k.dim() != 4:
+        raise ValueError("k must be [B,H,T,d]")
+    B, H, d, T = cache.B, cache.H, cache.d, k.shape[2]
+    ks, vs = _rows(k, "k", (B, H, T, d), cache.dtype), _rows(v, "v", (B, H, T, d), cache.dtype)
+    qs, Hq = (0, 0, 0), 0
+    if q is not None:
+        if q.dim() != 4:
+            raise ValueError("q must be [B,Hq,T,d]")
+        Hq = q.shape[1]
+        qs = _rows(q, "q", (B, Hq, T, d), cache.dtype)
+        if q_out is None:
+            q_out = torch.empty((B, Hq, T, d), dtype=q.dtype, device=q.device)
+        _expect(q_out, "q_out", (B, Hq, T, d), cache.dtype)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _expect(counts, "counts", (B,), torch.int64)
+    _expect(mass, "mass", (B, H, T), torch.float32)
+    _contig(counts, mass, q_out)
+    cache.here(k, v, q, q_out, counts, mass)
+    p = [None if t is None else t.data_ptr() for t in (q, counts, mass, q_out)]
+    a = AppendArgs(T, Hq, p[0], k.data_ptr(), v.data_ptr(), _I3(*qs), _I3(*ks), _I3(*vs), p[1], p[2], p[3])
+    _check(_lib.tc_cache_append(cache.ref, None if rotary is None else rotary.ref, ctypes.byref(a),
+                                _raw_stream(stream)), "tc_cache_append")
+    return q_out
+
+
+def cache_attend_workspace(cache: PagedCache, Hq: int, *, accumulate: bool = False) -> torch.Tensor:
+    """A workspace for cache_attend on this cache (one per concurrent stream)."""
+    n = _lib.tc_cache_attend_workspace_size(cache.ref, int(Hq), TC_CACHE_ACCUMULATE if accumulate else 0)
+    return _new_workspace(n, "tc_cache_attend_workspace_size", cache)
+
+
+def cache_attend(cache: PagedCache, q: torch.Tensor, *, g: Optional[torch.Tensor] = None,
+                 accumulate: bool = False, y: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """tc_cache_attend: attention of one token per row, q [B,Hq,d] (rotated),
+    over the row's pairs, plus sigmoid(g) q A when g [Hq] float32 is given.
+    accumulate adds each pair's weight to the cache's mass.  Returns y
+    [B,Hq,d]; rows that are empty (negative length) are not written."""
+    Hq = _query_heads(cache, q)
+    _expect(g, "g", (Hq,), torch.float32)
+    if g is not None and cache.A is None:
+        raise ValueError("g reads the memory, but the cache has none")
+    if accumulate and cache.mass is None:
+        raise ValueError("accumulate needs a cache with mass")
+    if y is None:
+        y = torch.empty_like(q)
+    _expect(y, "y", q.shape, cache.dtype)
+    flags = TC_CACHE_ACCUMULATE if accumulate else 0
+    n = 0 if workspace is not None else _lib.tc_cache_attend_workspace_size(cache.ref, Hq, flags)
+    workspace, room = _workspace(n, "tc_cache_attend_workspace_size", workspace, cache.device)
+    _contig(q, g, y)
+    cache.here(q, g, y, workspace)
+    _check(_lib.tc_cache_attend(cache.ref, Hq, q.data_ptr(), None if g is None else g.data_ptr(), y.data_ptr(),
+                                flags, workspace.data_ptr(), room, _raw_stream(stream)), "tc_cache_attend")
+    return y
+
+
+def _query_heads(cache: PagedCache, q: torch.Tensor) -> int:
+    if q.dim() != 3:
+        raise ValueError("q must be [B,Hq,d]")
+    Hq = q.shape[1]
+    _expect(q, "q", (cache.B, Hq, cache.d), cache.dtype)
+    if Hq < 1 or Hq % cache.H:
+        raise ValueError(f"{Hq} query heads over {cache.H} key/value heads")
+    return Hq
+
+
+def cache_evict_workspace(cache: PagedCache) -> torch.Tensor:
+    """A workspace for cache_evict on this cache (one per concurrent stream)."""
+    return _new_workspace(_lib.tc_cache_evict_workspace_size(cache.ref), "tc_cache_evict_workspace_size", cache)
+
+
+def cache_evict(cache: PagedCache, budget: int, *, recent: int = 1,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """tc_cache_evict: every row that holds more than budget pairs loses its
+    least attended ones (per head), which are written into the memory A; the
+    pairs of the last `recent` positions go last."""
+    if cache.mass is None:
+        raise ValueError("eviction needs a cache with mass and pos")
+    n = 0 if workspace is not None else _lib.tc_cache_evict_workspace_size(cache.ref)
+    workspace, room = _workspace(n, "tc_cache_evict_workspace_size", workspace, cache.device)
+    cache.here(workspace)
+    _check(_lib.tc_cache_evict(cache.ref, int(budget), int(recent), workspace.data_ptr(), room,
+                               _raw_stream(stream)), "tc_cache_evict")
+
+
+def cache_step_workspace(cache: PagedCache, Hq: int, *, accumulate: bool = True) -> torch.Tensor:
+    """A workspace for cache_step on this cache (one per concurrent stream)."""
+    n = _lib.tc_cache_step_workspace_size(cache.ref, int(Hq), TC_CACHE_ACCUMULATE if accumulate else 0)
+    return _new_workspace(n, "tc_cache_step_workspace_size", cache)
+
+
+def cache_step(cache: PagedCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, budget: int, *,
+               rotary: Optional[Rotary] = None, recent: int = 1, g: Optional[torch.Tensor] = None,
+               accumulate: bool = True, y: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """tc_cache_step: one serving step of every row, in the layer's order: the
+    token's pair k, v [B,H,d] enters (rotated), the least attended pair beyond
+    budget leaves into the memory, and q [B,Hq,d] (rotated here) reads both.
+    q, k and v may have any strides with a contiguous head dimension.  Returns
+    y [B,Hq,d]."""
+    Hq = _query_heads(cache, q)
+    qs, ks, vs = (_token_rows(t, n, (cache.B, h, cache.d), cache.dtype)
+                  for t, n, h in ((q, "q", Hq), (k, "k", cache.H), (v, "v", cache.H)))
+    _expect(g, "g", (Hq,), torch.float32)
+    if g is not None and cache.A is None:
+        raise ValueError("g reads the memory, but the cache has none")
+    if cache.mass is None:
+        raise ValueError("a step needs a cache with mass and pos")
+    if y is None:
+        y = torch.empty((cache.B, Hq, cache.d), dtype=cache.dtype, device=q.device)
+    _expect(y, "y", q.shape, cache.dtype)
+    flags = TC_CACHE_ACCUMULATE if accumulate else 0
+    n = 0 if workspace is not None else _lib.tc_cache_step_workspace_size(cache.ref, Hq, flags)
+    workspace, room = _workspace(n, "tc_cache_step_workspace_size", workspace, cache.device)
+    _contig(g, y)
+    cache.here(q, k, v, g, y, workspace)
+    a = StepArgs(Hq, q.data_ptr(), k.data_ptr(), v.data_ptr(), _I2(*qs), _I2(*ks), _I2(*vs),
+                 None if g is None else g.data_ptr(), y.data_ptr(), int(budget), int(recent), flags)
+    _check(_lib.tc_cache_step(cache.ref, None if rotary is None else rotary.ref, ctypes.byref(a),
+                              workspace.data_ptr(), room, _raw_stream(stream)), "tc_cache_step")
     return y
 
 

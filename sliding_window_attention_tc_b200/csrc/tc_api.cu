@@ -193,6 +193,12 @@ tc_status check_decode_state(const tc_decode_state *s) {
 }  // namespace
 
 namespace tc {
+tc_status api_current_device(int *dev, int *num_sms) { return current_device(dev, num_sms); }
+bool api_device_ptr(const void *p, int dev) { return is_device_ptr(p, dev); }
+int api_sm_count() { return sm_count_or_default(); }
+int *api_status_ptr() { return status_ptr(); }
+unsigned long long api_wait_limit_ns() { return wait_limit_ns(); }
+
 ScopedPrefillPath::ScopedPrefillPath(int path) : prev(t_path_override) { t_path_override = path; }
 ScopedPrefillPath::~ScopedPrefillPath() { t_path_override = prev; }
 }  // namespace tc

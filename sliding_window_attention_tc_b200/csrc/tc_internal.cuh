@@ -213,6 +213,14 @@ size_t sm100_workspace_bytes(const tc_prefill_desc &d, int num_sms, bool varlen 
 cudaError_t launch_prefill_sm100(const PrefillParams &p, int num_sms, cudaStream_t s);
 int sm100_launch_count(const tc_prefill_desc &d);
 
+// tc_api.cu: the checks and process-wide settings that entry points of other
+// files share.
+tc_status api_current_device(int *dev, int *num_sms);   // TC_OK on an sm_100 device
+bool api_device_ptr(const void *p, int dev);            // memory that a kernel on dev may use
+int api_sm_count();                                     // of the current device; 148 without one
+int *api_status_ptr();                                  // the device status word
+unsigned long long api_wait_limit_ns();
+
 // tc_api.cu: a per-thread override of tc_set_prefill_path (TC_PATH_*, or -1
 // for none) for the calls this thread makes while the object lives.
 struct ScopedPrefillPath {
