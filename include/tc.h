@@ -511,7 +511,8 @@ TC_API tc_status tc_cache_append(const tc_paged_cache *cache, const tc_rotary *r
  * A row that holds no pair gives the memory's read alone.  With
  * TC_CACHE_ACCUMULATE mass_j grows by the sum of p_j over the heads that share
  * the key/value head.
- *   q, y [B,Hq,d] contiguous, Hq a multiple of H, Hq/H <= 128; g [Hq] float32, NULL exactly
+ *   q, y [B,Hq,d] contiguous, Hq a multiple of H, Hq/H <= 128,
+ *   B Hq max_pages page < 2^38; g [Hq] float32, NULL exactly
  *   when cache->A is NULL or the memory is not to be read.
  * Work is split over the lengths and joined: two launches.  Every sum has a
  * fixed order on a given device.  Workspace:
@@ -537,9 +538,12 @@ TC_API size_t tc_cache_evict_workspace_size(const tc_paged_cache *cache);
 TC_API tc_status tc_cache_evict(const tc_paged_cache *cache, int64_t budget, int64_t recent,
                                 void *workspace, size_t workspace_bytes, tc_stream_t stream);
 
-/* One serving step for every row, in the order of Fig. 2: tc_cache_append of
- * one token, tc_cache_evict down to budget, tc_cache_attend with the token's
- * query; the same results in three launches.
+/* One serving step for every row, in the order of Fig. 2: the token's pair
+ * enters, one pair leaves if the row then holds more than budget, the token's
+ * query reads both.  For rows that held at most budget pairs these are the
+ * results of tc_cache_append, tc_cache_evict and tc_cache_attend, in three
+ * launches; a row above its budget (after a lower one was chosen) stays above
+ * it by as much until tc_cache_evict is called.
  *   q [B,Hq,d], k, v [B,H,d]: not rotated (rotary NULL: used as they are);
  *   strides in elements of b and h (slices of a fused projection), the head
  *   dimension contiguous, the alignment of their type; y [B,Hq,d] contiguous.

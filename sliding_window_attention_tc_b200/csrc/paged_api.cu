@@ -137,6 +137,7 @@ CacheParams cache_params(const tc_paged_cache *c) {
     p.n_pages = (int)c->n_pages;
     p.max_pages = (int)c->max_pages;
     p.status = api_status_ptr();
+    p.page_mul = ((uint64_t(1) << 40) + c->page - 1) / c->page;
     return p;
 }
 
@@ -154,21 +155,22 @@ struct AttendRoom {
 // Workspace of an eviction: what each row holds afterwards, sorting room.
 struct EvictRoom {
     size_t row_len, sort, bytes;
-    explicit EvictRoom(const tc_paged_cache *c) {
+    EvictRoom(const tc_paged_cache *c, int sms) {
         row_len = 0;
         sort = round_up((size_t)c->B * 8);
-        bytes = sort + round_up(evict_sort_bytes(c->B * c->H, c->max_pages * c->page));
+        bytes = sort + round_up(evict_sort_bytes(c->B * c->H, (int)c->d, c->max_pages * c->page, sms));
     }
 };
 
-// Workspace of a step: the eviction's, the rotated queries, their reads of A,
-// the attention's.
+// Workspace of a step: what each row holds afterwards, the rotated queries,
+// their reads of A, the attention's.
 struct StepRoom {
-    size_t q, memo, attend, bytes;
+    size_t row_len, q, memo, attend, bytes;
     int slices;
     StepRoom(const tc_paged_cache *c, int64_t Hq, uint32_t flags, int sms) {
-        slices = evict_slices(c->B * c->H, (int)c->d, c->max_pages * c->page, sms);
-        q = EvictRoom(c).bytes;
+        slices = evict_slices(c->B * c->H, (int)c->d, sms);
+        row_len = 0;
+        q = round_up((size_t)c->B * 8);
         memo = q + round_up((size_t)(c->B * Hq * c->d) * elem(c->dtype));
         attend = memo + (c->A ? round_up((size_t)(c->B * Hq * c->d) * (size_t)slices * 4) : 0);
         bytes = attend + AttendRoom(c, Hq, flags, sms).bytes;
@@ -180,7 +182,12 @@ tc_status check_attend(const tc_paged_cache *c, int64_t Hq, uint32_t flags) {
     if (st != TC_OK) return st;
     if (flags & ~TC_CACHE_ACCUMULATE) return TC_ERR_INVALID_ARG;
     if ((flags & TC_CACHE_ACCUMULATE) && !c->mass) return TC_ERR_INVALID_ARG;
-    return check_heads(c, Hq);
+    st = check_heads(c, Hq);
+    if (st != TC_OK) return st;
+    const int heads = attend_heads_per_item((int)(Hq / c->H), c->dtype);
+    const double items = (double)((Hq / c->H + heads - 1) / heads);
+    // units of work are counted in 31 bits
+    return attend_units((double)c->B * (double)c->H * items, c->max_pages * c->page) < 2147483648.0 ? TC_OK : TC_ERR_UNSUPPORTED;
 }
 
 AttendParams attend_params(const tc_paged_cache *c, int64_t Hq, const float *g, void *y, uint32_t flags, char *ws, int sms) {
@@ -194,7 +201,7 @@ AttendParams attend_params(const tc_paged_cache *c, int64_t Hq, const float *g, 
     p.d = (int)c->d;
     p.heads = attend_heads_per_item(p.G, c->dtype);
     p.items = (p.G + p.heads - 1) / p.heads;
-    p.prefix = reinterpret_cast<int64_t *>(ws + room.prefix);
+    p.prefix = reinterpret_cast<int *>(ws + room.prefix);
     p.part = reinterpret_cast<float *>(ws + room.part);
     p.z = (flags & TC_CACHE_ACCUMULATE) ? reinterpret_cast<float *>(ws + room.z) : nullptr;
     p.wait_ns = api_wait_limit_ns();
@@ -324,7 +331,7 @@ tc_status tc_cache_attend(const tc_paged_cache *c, int64_t Hq, const void *q, co
 
 size_t tc_cache_evict_workspace_size(const tc_paged_cache *c) {
     if (check_cache(c) != TC_OK || !c->mass) return (size_t)-1;
-    return EvictRoom(c).bytes;
+    return EvictRoom(c, api_sm_count()).bytes;
 }
 
 tc_status tc_cache_evict(const tc_paged_cache *c, int64_t budget, int64_t recent, void *workspace, size_t workspace_bytes,
@@ -335,7 +342,7 @@ tc_status tc_cache_evict(const tc_paged_cache *c, int64_t budget, int64_t recent
     int dev = 0, sms = 0;
     st = api_current_device(&dev, &sms);
     if (st != TC_OK) return st;
-    const EvictRoom room(c);
+    const EvictRoom room(c, sms);
     if (!workspace || workspace_bytes < room.bytes) return TC_ERR_WORKSPACE;
     if (!cache_on_device(c, dev) || !api_device_ptr(workspace, dev)) return TC_ERR_INVALID_ARG;
     char *ws = static_cast<char *>(workspace);
@@ -346,9 +353,8 @@ tc_status tc_cache_evict(const tc_paged_cache *c, int64_t budget, int64_t recent
     p.row_len = reinterpret_cast<int64_t *>(ws + room.row_len);
     p.sort_ws = reinterpret_cast<unsigned char *>(ws + room.sort);
     p.Hq = (int)c->H;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_cache_evict(p, c->dtype, (int)c->d, false, evict_slices(c->B * c->H, (int)c->d, c->max_pages * c->page, sms), s);
-    if (e == cudaSuccess) e = launch_cache_evict_finish(p, s);
+    p.wait_ns = api_wait_limit_ns();
+    const cudaError_t e = launch_cache_evict(p, c->dtype, (int)c->d, sms, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? TC_OK : TC_ERR_CUDA;
 }
 
@@ -386,12 +392,11 @@ tc_status tc_cache_step(const tc_paged_cache *c, const tc_rotary *rotary, const 
     for (const void *x : ptrs)
         if (x && !api_device_ptr(x, dev)) return TC_ERR_INVALID_ARG;
     char *ws = static_cast<char *>(workspace);
-    const EvictRoom er(c);
     e.c = cache_params(c);
     e.budget = a->budget;
     e.recent = a->recent;
-    e.row_len = reinterpret_cast<int64_t *>(ws + er.row_len);
-    e.sort_ws = reinterpret_cast<unsigned char *>(ws + er.sort);
+    e.row_len = reinterpret_cast<int64_t *>(ws + room.row_len);
+    e.wait_ns = api_wait_limit_ns();
     e.q = a->q;
     e.k_new = a->k;
     e.v_new = a->v;
@@ -404,7 +409,7 @@ tc_status tc_cache_step(const tc_paged_cache *c, const tc_rotary *rotary, const 
     e.memo = a->g ? reinterpret_cast<float *>(ws + room.memo) : nullptr;
     e.Hq = (int)a->Hq;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (launch_cache_evict(e, c->dtype, (int)c->d, true, room.slices, s) != cudaSuccess) return TC_ERR_CUDA;
+    if (launch_cache_step_insert(e, c->dtype, (int)c->d, room.slices, s) != cudaSuccess) return TC_ERR_CUDA;
     AttendParams p = attend_params(c, a->Hq, a->g, a->y, a->flags, ws + room.attend, sms);
     p.q = e.q_rot;
     p.row_len = e.row_len;

@@ -4,7 +4,7 @@
 //   y_h = sum_j p_j v_j + sigmoid(g_h) q_h A,  p = softmax_j(<q_h,k_j>/sqrt(d))
 //
 // Bound by memory: every key and value is read once per group of query heads.
-// The work, tiles of 64 pairs of one (row, key/value head, group of query
+// The work, tiles of 128 pairs of one (row, key/value head, group of query
 // heads), is laid end to end and cut into equal parts, one per block, wherever
 // the rows begin and end: rows of any lengths keep every SM equally busy.  A
 // block walks its part with a running maximum and sum; at the end of a row's
@@ -12,10 +12,10 @@
 // of each row's stretches, the memory's read, and (from the scores the first
 // kernel left in the workspace) the weights.
 //
-// bf16: each of the four warps takes 16 pairs of a tile, on its own: its own
-// ring of TMA loads (16 x d boxes, swizzled; a page holds a multiple of 16
-// pairs), its own running statistics; no barrier between warps until a row's
-// stretch ends.  Products run as S^T = K Q^T (16 pairs x 8 heads) and
+// bf16: each of the four warps takes 32 pairs of a tile, on its own: its own
+// place in a ring of TMA loads (boxes of 32 rows, or 16 where a page's end may fall between;
+// swizzled), brought in by a lane of a fifth warp, and its own running
+// statistics; no barrier between warps until a row's stretch ends.  Products run as S^T = K Q^T (16 pairs x 8 heads) and
 // O^T = V^T P^T with m16n8k16: with the pairs as M, eight heads fill a product
 // that would be half empty with the heads as M, and the same lanes hold a
 // head's scores and its outputs, so rescaling needs no exchange.  P enters as a
@@ -37,10 +37,11 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTile = 64;        // pairs per tile
-constexpr int kThreads = 128;    // first kernel
-constexpr int kWarps = 4;
-constexpr int kWarpPairs = 16;   // pairs of a tile one warp takes
+constexpr int kTile = 128;       // pairs per tile
+constexpr int kWarps = 4;        // warps that compute, in the first kernel
+constexpr int kThreads = kWarps * 32;
+constexpr int kWarpPairs = 32;   // pairs of a tile one warp takes
+constexpr int kBox = 16;         // pairs that always share a page
 constexpr int kJoinThreads = 256;
 
 __device__ __forceinline__ int64_t row_pairs(const AttendParams &p, int b) {
@@ -51,72 +52,93 @@ __device__ __forceinline__ int row_tiles(const AttendParams &p, int b) {
     return (int)((row_pairs(p, b) + kTile - 1) / kTile);
 }
 
-// Position in the laid-out work: unit u is tile `tile` of item `item` of row b.
+// A place in the laid-out work, and the stretch of tiles from there on that
+// belongs to one (row, item): tiles .. of it are this block's.
 struct Cursor {
-    int64_t left;  // units until the end of the part, this one included
-    int b, item, tile, tiles;
-    int64_t n;     // pairs of row b
+    int left;      // units until the end of the part, from the stretch's first
+    int b, item, tile, tiles;  // row, item of it, first tile, tiles a row's item has
+    int n;         // pairs of row b
+    int count;     // tiles of the stretch
 
     __device__ __forceinline__ void enter_row(const AttendParams &p) {
-        n = row_pairs(p, b);
-        tiles = (int)((n + kTile - 1) / kTile);
+        n = (int)row_pairs(p, b);
+        tiles = (n + kTile - 1) / kTile;
     }
-    // `per_row`: items a row has
-    __device__ __forceinline__ void next(const AttendParams &p, int per_row) {
-        if (--left == 0) return;
-        if (++tile < tiles) return;
+    __device__ __forceinline__ void measure() { count = min(tiles - tile, left); }
+    // on to the next stretch; false at the part's end
+    __device__ __forceinline__ bool next(const AttendParams &p, int per_row) {
+        left -= count;
+        if (left == 0) return false;
         tile = 0;
-        if (++item < per_row) return;
-        item = 0;
-        do {
-            ++b;
-            enter_row(p);
-        } while (tiles == 0);  // left > 0: a row with tiles follows
+        if (++item == per_row) {
+            item = 0;
+            do {
+                ++b;
+                enter_row(p);
+            } while (tiles == 0);  // left > 0: a row with tiles follows
+        }
+        measure();
+        return true;
     }
 };
 
-// This block's part of total = per_row * (tiles of all rows) units, cut evenly
-// over min(gridDim.x, total) blocks.  Every block adds up the rows' tiles by
-// itself; block 0 of the first kernel also stores them (prefix) for the join.
-// Returns false when there is nothing to do.  Block-wide.
-__device__ bool find_part(const AttendParams &p, int per_row, Cursor &cur) {
-    __shared__ int64_t s_sum[kWarps];
-    __shared__ int64_t s_off;
-    __shared__ int s_row;
+// total units cut over G = min(grid, total) blocks: the first `more` of them
+// have per + 1, the others per.  (Units fit 31 bits: checked on the host.)
+struct Cut {
+    uint32_t G, per, more;
+    __device__ __forceinline__ Cut(uint32_t total, uint32_t grid) {
+        G = total < grid ? total : grid;
+        per = G ? total / G : 0;
+        more = total - per * G;
+    }
+    __device__ __forceinline__ uint32_t begin(uint32_t block) const { return block * per + min(block, more); }
+    // the block that has unit u
+    __device__ __forceinline__ uint32_t block_of(uint32_t u) const {
+        const uint32_t x = more * (per + 1);
+        return u < x ? u / (per + 1) : more + (u - x) / per;
+    }
+};
+
+// This block's part of the per_row * (tiles of all rows) units.  Every block
+// adds up the rows' tiles by itself; block 0 also stores them (prefix) for the
+// join.  Returns false when there is nothing to do.  Block-wide; WARPS warps.
+template <int WARPS>
+__device__ __forceinline__ bool find_part(const AttendParams &p, int per_row, Cursor &cur) {
+    __shared__ int s_sum[WARPS];
+    __shared__ int s_off, s_row;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.c.B;
-    const int per = (B + kThreads - 1) / kThreads;
+    const int per = (B + WARPS * 32 - 1) / (WARPS * 32);
     const int b0 = tid * per, b1 = min(B, b0 + per);
-    int64_t mine = 0;
+    int mine = 0;
     for (int b = b0; b < b1; ++b) mine += row_tiles(p, b);
-    int64_t v = mine;
+    int v = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += y;
     }
     if (lane == 31) s_sum[warp] = v;
     __syncthreads();
-    int64_t before = 0, all = 0;
+    int before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += s_sum[w];
         all += s_sum[w];
     }
     before += v - mine;
     if (blockIdx.x == 0) {
-        int64_t x = before;
+        int x = before;
         for (int b = b0; b < b1; ++b) {
             p.prefix[b] = x;
             x += row_tiles(p, b);
         }
         if (tid == 0) p.prefix[B] = all;
     }
-    const int64_t total = all * per_row, G = total < gridDim.x ? total : gridDim.x;
-    if (blockIdx.x >= G) return false;
-    const int64_t u0 = blockIdx.x * total / G, u1 = (blockIdx.x + 1) * total / G;
+    const Cut cut((uint32_t)all * per_row, gridDim.x);
+    if (blockIdx.x >= cut.G) return false;
+    const int u0 = (int)cut.begin(blockIdx.x), u1 = (int)cut.begin(blockIdx.x + 1);
     if (u0 >= before * per_row && u0 < (before + mine) * per_row) {
-        int64_t x = before;
-        int b = b0;
+        int x = before, b = b0;
         for (;; ++b) {
             const int t = row_tiles(p, b);
             if (u0 < (x + t) * per_row) break;
@@ -128,28 +150,38 @@ __device__ bool find_part(const AttendParams &p, int per_row, Cursor &cur) {
     __syncthreads();
     cur.b = s_row;
     cur.enter_row(p);
-    cur.item = (int)(s_off / cur.tiles);
-    cur.tile = (int)(s_off % cur.tiles);
+    cur.item = s_off / cur.tiles;
+    cur.tile = s_off - cur.item * cur.tiles;
     cur.left = u1 - u0;
+    cur.measure();
     return true;
 }
 
 // Partial results: the slot of (block, item) is block + item's number, which
-// grows by at least one along the work, so no two share one.
-__host__ __device__ inline int64_t part_floats(int heads, int d) { return (int64_t)heads * (d + 2); }
+// grows by at least one along the work, so no two share one.  O [heads][d],
+// then (m, l) per head, in whole 16-byte vectors.
+__host__ __device__ inline int64_t part_floats(int heads, int d) { return ((int64_t)heads * (d + 2) + 3) / 4 * 4; }
 
 // ---- bf16 -----------------------------------------------------------------------
 
-// Byte offset of 16-byte chunk c of row r in a 16-row tile of d bf16, as TMA
-// writes it with the widest swizzle a row allows (boxes of at most 64 columns).
+// A warp's 32 rows of d bf16 in shared memory: boxes of at most 64 columns, in
+// each the rows one after the other, swizzled as TMA does it with the widest
+// pattern a row allows.  lane_offset is the place of (row r, 16-byte chunk hi)
+// of a 16-row half; k-step k (chunk 2k + hi) lies at that place with k's low
+// bits flipped in, because the swizzle is an exclusive or.
 template <int D>
-__device__ __forceinline__ uint32_t tile_offset(int r, int c) {
-    constexpr int RB = D >= 64 ? 128 : D * 2;  // bytes of a box row
-    constexpr int CPR = RB / 16;
-    const int box = c / CPR, cc = c % CPR;
-    const int x = RB == 128 ? (r & 7) : RB == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
-    return box * (16 * RB) + r * RB + ((cc ^ x) << 4);
-}
+struct TileLayout {
+    static constexpr int RB = D >= 64 ? 128 : D * 2;   // bytes of a box row
+    static constexpr int BOX = kWarpPairs * RB;        // bytes of a box
+    static constexpr int KPB = RB / 32;                // k-steps of a box
+    __device__ __forceinline__ static uint32_t lane_offset(int r, int hi) {
+        const int x = RB == 128 ? (r & 7) : RB == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
+        return r * RB + ((hi ^ x) << 4);
+    }
+    __device__ __forceinline__ static uint32_t at(uint32_t lane, int k) {
+        return (lane ^ ((k % KPB) << 5)) + (k / KPB) * BOX;
+    }
+};
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -188,96 +220,148 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
 
 template <int D, int NT>
 struct Bf16Shape {
-    static constexpr int STAGES = D == 128 ? (NT == 1 ? 3 : 2) : 4;
-    static constexpr int STAGE_BYTES = 16 * D * 2 * 2;  // one warp's keys and values
+    static constexpr int STAGES = D >= 64 ? 3 : 4;
+    static constexpr int STAGE_BYTES = kWarpPairs * D * 2 * 2;  // one warp's keys and values
     static constexpr int HEADS = 8 * NT;
     static constexpr int OS = D + 4;                    // floats between heads of a warp's outputs
     static constexpr int RING = kWarps * STAGES * STAGE_BYTES;
     static constexpr int SMEM = 1024 + RING + 2 * HEADS * OS * 4;
 };
 
+// What a stage holds for a warp: the pool rows of its two halves, and their
+// pairs (0: nothing was loaded).
+struct StageNote {
+    int row[2];
+    int pairs[2];
+};
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) attend_bf16_kernel(const __grid_constant__ CUtensorMap map_k,
-                                                               const __grid_constant__ CUtensorMap map_v,
-                                                               const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(kThreads + 32) attend_bf16_kernel(const __grid_constant__ CUtensorMap map_k,
+                                                                    const __grid_constant__ CUtensorMap map_v,
+                                                                    const __grid_constant__ AttendParams p, int box_rows) {
     using S = Bf16Shape<D, NT>;
+    using L = TileLayout<D>;
     constexpr int KS = D / 16;      // k-steps of a score, 16-wide blocks of the output
-    constexpr int BOX = D >= 64 ? 64 : D;
+    constexpr int HALF = kBox * L::RB;
     extern __shared__ unsigned char dyn[];
-    __shared__ __align__(8) uint64_t s_bar[kWarps][S::STAGES];
+    __shared__ __align__(8) uint64_t s_full[S::STAGES], s_free[S::STAGES];
+    __shared__ StageNote s_note[S::STAGES][kWarps];
     __shared__ float s_m[kWarps][S::HEADS], s_l[kWarps][S::HEADS];
     __shared__ int s_abort;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (lane == 0)
-        for (int s = 0; s < S::STAGES; ++s) mbar_init(&s_bar[warp][s], 1);
-    if (tid == 0) s_abort = 0;
-    fence_mbar_init();
+    if (tid == 0) {
+        for (int s = 0; s < S::STAGES; ++s) {
+            mbar_init(&s_full[s], kWarps);
+            mbar_init(&s_free[s], kWarps);
+        }
+        s_abort = 0;
+        fence_mbar_init();
+    }
+    if (tid == kThreads) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+    }
     griddep_wait();
     griddep_launch_dependents();
     const int per_row = p.c.H * p.items;
     Cursor cur;
-    const bool any = find_part(p, per_row, cur);  // its barrier also publishes the mbarriers
-    if (!any) return;
-    __syncthreads();
+    if (!find_part<kWarps + 1>(p, per_row, cur)) return;  // its barriers also publish the mbarriers
 
     const uint32_t dyn0 = (smem_u32(dyn) + 1023u) & ~1023u;
-    const uint32_t ring = dyn0 + warp * S::STAGES * S::STAGE_BYTES;
-    float *s_o = reinterpret_cast<float *>(dyn + (dyn0 - smem_u32(dyn)) + S::RING);  // [2][HEADS][OS]
-
-    Cursor ahead = cur;
-    int ahead_page = -1;  // table entry of the next load, fetched one step early
-    auto fetch_page = [&]() {
-        const int64_t j0 = (int64_t)ahead.tile * kTile + warp * kWarpPairs;
-        if (ahead.left > 0 && j0 < ahead.n) ahead_page = p.c.table[(int64_t)ahead.b * p.c.max_pages + j0 / p.c.page];
-    };
-    fetch_page();
-    uint32_t valid = 0;   // pairs in each stage, 8 bits each
-    // loads the next tile's 16 pairs into a stage, and moves on
-    auto issue = [&](int st) {
-        valid &= ~(0xffu << (8 * st));
-        if (ahead.left <= 0) return;
-        const int64_t j0 = (int64_t)ahead.tile * kTile + warp * kWarpPairs;
-        if (j0 < ahead.n) {
-            if (page_ok(p.c, ahead_page)) {
-                valid |= (uint32_t)min((int64_t)kWarpPairs, ahead.n - j0) << (8 * st);
-                if (lane == 0) {
-                    const int row = (int)pool_row(p.c, ahead_page, ahead.item / p.items, (int)(j0 % p.c.page));
-                    uint64_t *bar = &s_bar[warp][st];
-                    const uint32_t dst = ring + st * S::STAGE_BYTES;
-                    mbar_expect_tx(bar, S::STAGE_BYTES);
-#pragma unroll
-                    for (int x = 0; x < D; x += BOX) {
-                        tma_load_2d(dst + x * 32, &map_k, bar, x, row);
-                        tma_load_2d(dst + 32 * D + x * 32, &map_v, bar, x, row);
-                    }
-                }
-            } else if (lane == 0) {
+    if (warp == kWarps) {
+        // ---- loads: lane w brings in warp w's 32 pairs of every tile ---------------------
+        if (lane >= kWarps) return;
+        const int w = lane;
+        const bool whole = box_rows == kWarpPairs;  // one box holds both halves: a page does
+        int page0 = -1, page1 = -1;                 // table entries, fetched a tile early
+        int j = cur.tile * kTile + w * kWarpPairs, left = cur.count;
+        const int32_t *table = p.c.table + (int64_t)cur.b * p.c.max_pages;
+        int head = (cur.item / p.items) * p.c.page;
+        auto fetch_pages = [&]() {
+            if (j < cur.n) page0 = table[p.c.page_of(j)];
+            if (j + kBox < cur.n) page1 = table[p.c.page_of(j + kBox)];
+        };
+        fetch_pages();
+        int st = 0;
+        uint32_t round = 0;  // times the ring went around
+        bool dead = false;
+        for (bool more = true; more;) {
+            if (round > 0 && !mbar_wait(&s_free[st], (round - 1) & 1u, &s_abort, p.c.status, p.wait_ns)) {
+                dead = true;
+                break;
+            }
+            int n0 = max(0, min(kBox, cur.n - j)), n1 = max(0, min(kBox, cur.n - j - kBox));
+            if ((n0 && !page_ok(p.c, page0)) || (n1 && !page_ok(p.c, page1))) {
                 report(p.c.status, TC_ERR_DEVICE_BOUNDS);
+                if (!page_ok(p.c, page0)) n0 = 0;
+                if (!page_ok(p.c, page1)) n1 = 0;
+            }
+            const int step = p.c.H * p.c.page;
+            const int r0 = page0 * step + head + j - p.c.page_of(j) * p.c.page;
+            const int r1 = page1 * step + head + j + kBox - p.c.page_of(j + kBox) * p.c.page;
+            uint64_t *bar = &s_full[st];
+            s_note[st][w] = StageNote{{r0, r1}, {n0, n1}};
+            const uint32_t dst = dyn0 + (w * S::STAGES + st) * S::STAGE_BYTES;
+            if (n0 | n1) mbar_expect_tx(bar, whole ? S::STAGE_BYTES : ((n0 ? 1 : 0) + (n1 ? 1 : 0)) * (S::STAGE_BYTES / 2));
+            else mbar_arrive(bar);
+#pragma unroll
+            for (int x = 0; x * L::RB < D * 2; ++x) {
+                const uint32_t kd = dst + x * L::BOX, vd = kd + S::STAGE_BYTES / 2;
+                if (n0 || (whole && n1)) {
+                    tma_load_2d(kd, &map_k, bar, x * 64, r0);
+                    tma_load_2d(vd, &map_v, bar, x * 64, r0);
+                }
+                if (!whole && n1) {
+                    tma_load_2d(kd + HALF, &map_k, bar, x * 64, r1);
+                    tma_load_2d(vd + HALF, &map_v, bar, x * 64, r1);
+                }
+            }
+            j += kTile;
+            if (--left == 0) {
+                more = cur.next(p, per_row);
+                j = cur.tile * kTile + w * kWarpPairs;
+                left = cur.count;
+                table = p.c.table + (int64_t)cur.b * p.c.max_pages;
+                head = (cur.item / p.items) * p.c.page;
+            }
+            if (more) fetch_pages();
+            if (++st == S::STAGES) {
+                st = 0;
+                ++round;
             }
         }
-        ahead.next(p, per_row);
-        fetch_page();
-    };
-#pragma unroll
-    for (int s = 0; s < S::STAGES; ++s) issue(s);
+        // after a wait that ran out: no copy may land once the block is gone
+        if (dead)
+            for (int s = 0; s < S::STAGES; ++s) {
+                const uint32_t uses = round + (s < st ? 1 : 0);  // loads into stage s so far
+                if (uses) mbar_wait_drain(&s_full[s], (uses - 1) & 1u);
+            }
+        return;
+    }
 
+    const uint32_t ring = dyn0 + warp * S::STAGES * S::STAGE_BYTES;
+    float *s_o = reinterpret_cast<float *>(dyn + (dyn0 - smem_u32(dyn)) + S::RING);  // [2][HEADS][OS]
+    auto warps_sync = []() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
     const float scale = rsqrtf((float)D) * 1.4426950408889634f;  // log2(e)/sqrt(d)
-    uint32_t phase = 0;  // parity of each stage's next completion
+    const uint32_t k_lane = L::lane_offset((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+    const uint32_t v_lane = L::lane_offset((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
+    const int c0 = (lane % 4) * 2, r0 = lane / 4;  // this lane's columns (heads) and first row (pair)
+    uint32_t parity = 0;  // of the ring's round
     bool dead = false;
     int st = 0;
-    while (cur.left > 0) {
+    bool more = true;
+    while (more) {
         // ---- one stretch: tiles of one (row, head, group of query heads) -----------
-        const int b = cur.b, h = cur.item / p.items, grp = cur.item % p.items;
+        const int b = cur.b, h = cur.item / p.items, grp = cur.item - h * p.items;
         const int h0 = h * p.G + grp * S::HEADS;  // first query head
         const int heads = min(S::HEADS, p.G - grp * S::HEADS);
         const int64_t item = (int64_t)b * per_row + cur.item;
         uint32_t qf[NT][KS][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const int hh = t * 8 + lane / 4;
-            const uint32_t *qp = reinterpret_cast<const uint32_t *>(p.q) +
-                                 (((int64_t)b * p.Hq + h0 + hh) * D + (lane % 4) * 2) / 2;
+            const int hh = t * 8 + r0;
+            const uint32_t *qp = reinterpret_cast<const uint32_t *>(p.q) + (((int64_t)b * p.Hq + h0 + hh) * D + c0) / 2;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 qf[t][k][0] = hh < heads ? qp[k * 8] : 0u;
@@ -294,17 +378,13 @@ __global__ void __launch_bounds__(kThreads) attend_bf16_kernel(const __grid_cons
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[t][k][e] = 0.f;
         }
-        bool more = true;
-        while (more) {
-            const int64_t j0 = (int64_t)cur.tile * kTile + warp * kWarpPairs;
-            const int nv = (valid >> (8 * st)) & 0xff;
-            if (nv && !dead) {
-                if (!mbar_wait(&s_bar[warp][st], (phase >> st) & 1u, &s_abort, p.c.status, p.wait_ns)) dead = true;
-            }
-            if (nv && !dead) {
-                phase ^= 1u << st;
-                const uint32_t ks = ring + st * S::STAGE_BYTES, vs = ks + 32 * D;
-                // S^T = K Q^T, in two chains of products
+        for (int i = 0; i < cur.count; ++i) {
+            if (!dead && !mbar_wait(&s_full[st], parity, &s_abort, p.c.status, p.wait_ns)) dead = true;
+            if (dead) break;
+            const StageNote note = s_note[st][warp];
+            if (note.pairs[0] | note.pairs[1]) {
+                const uint32_t ks = ring + st * S::STAGE_BYTES, vs = ks + S::STAGE_BYTES / 2;
+                // S^T = K Q^T of both halves
                 float sc[NT][2][4];
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
@@ -312,39 +392,48 @@ __global__ void __launch_bounds__(kThreads) attend_bf16_kernel(const __grid_cons
                     for (int e = 0; e < 4; ++e) sc[t][0][e] = sc[t][1][e] = 0.f;
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    uint32_t a[4];
-                    ldsm_x4(ks + tile_offset<D>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4)), a);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) mma16816(sc[t][k & 1], a, qf[t][k][0], qf[t][k][1]);
+                    for (int f = 0; f < 2; ++f) {
+                        uint32_t a[4];
+                        ldsm_x4(ks + f * HALF + L::at(k_lane, k), a);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) mma16816(sc[t][f], a, qf[t][k][0], qf[t][k][1]);
+                    }
                 }
-                uint32_t ph[NT][2], pl[NT][2];
-                const int r0 = lane / 4, r1 = r0 + 8;  // this lane's pairs
+                uint32_t ph[NT][2][2], pl[NT][2][2];
                 bool grew = false;
                 float corr[NT][2];
+                const bool ragged = note.pairs[0] + note.pairs[1] < kWarpPairs;
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    float z[4];
+                    float z[2][4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) z[e] = (sc[t][0][e] + sc[t][1][e]) * scale;
-                    if (p.z) {
-                        // the group's scores of a pair lie side by side
-                        const int pg = p.c.table[(int64_t)b * p.c.max_pages + j0 / p.c.page];
-                        float *zr = p.z + pool_row(p.c, pg, h, (int)(j0 % p.c.page)) * p.G + grp * S::HEADS;
-                        const int c0 = t * 8 + (lane % 4) * 2;
-                        if (r0 < nv) {
-                            if (c0 < heads) zr[(int64_t)r0 * p.G + c0] = z[0];
-                            if (c0 + 1 < heads) zr[(int64_t)r0 * p.G + c0 + 1] = z[1];
+                    for (int f = 0; f < 2; ++f) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) z[f][e] = sc[t][f][e] * scale;
+                        if (p.z) {
+                            // the group's scores of a pair lie side by side
+                            float *zr = p.z + ((int64_t)note.row[f] + r0) * p.G + grp * S::HEADS + t * 8 + c0;
+                            if (p.G % 2 == 0) {
+                                if (t * 8 + c0 < heads) {
+                                    if (r0 < note.pairs[f]) *reinterpret_cast<float2 *>(zr) = make_float2(z[f][0], z[f][1]);
+                                    if (r0 + 8 < note.pairs[f]) *reinterpret_cast<float2 *>(zr + 8 * p.G) = make_float2(z[f][2], z[f][3]);
+                                }
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (t * 8 + c0 + (e & 1) < heads && r0 + (e >> 1) * 8 < note.pairs[f])
+                                        zr[(e & 1) + (e >> 1) * 8 * p.G] = z[f][e];
+                            }
                         }
-                        if (r1 < nv) {
-                            if (c0 < heads) zr[(int64_t)r1 * p.G + c0] = z[2];
-                            if (c0 + 1 < heads) zr[(int64_t)r1 * p.G + c0 + 1] = z[3];
+                        if (ragged) {
+                            if (r0 >= note.pairs[f]) z[f][0] = z[f][1] = -INFINITY;
+                            if (r0 + 8 >= note.pairs[f]) z[f][2] = z[f][3] = -INFINITY;
                         }
                     }
-                    if (r0 >= nv) z[0] = z[1] = -INFINITY;
-                    if (r1 >= nv) z[2] = z[3] = -INFINITY;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = fmaxf(z[e], z[e + 2]);
+                        float x = fmaxf(fmaxf(z[0][e], z[0][e + 2]), fmaxf(z[1][e], z[1][e + 2]));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -353,18 +442,24 @@ __global__ void __launch_bounds__(kThreads) attend_bf16_kernel(const __grid_cons
                         corr[t][e] = ex2(m[t][e] - ref);
                         grew |= mn > m[t][e];
                         m[t][e] = mn;
-                        z[e] = ex2(z[e] - ref);
-                        z[e + 2] = ex2(z[e + 2] - ref);
-                        l[t][e] = fmaf(l[t][e], corr[t][e], z[e] + z[e + 2]);
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            z[f][e] = ex2(z[f][e] - ref);
+                            z[f][e + 2] = ex2(z[f][e + 2] - ref);
+                        }
+                        l[t][e] = fmaf(l[t][e], corr[t][e], (z[0][e] + z[0][e + 2]) + (z[1][e] + z[1][e + 2]));
                     }
                     // P^T as a bf16 pair: hi rounded, lo the rest
-                    const uint32_t h01 = pack_bf16(z[0], z[1]), h23 = pack_bf16(z[2], z[3]);
-                    const uint32_t l01 = pack_bf16(z[0] - __uint_as_float(h01 << 16), z[1] - __uint_as_float(h01 & 0xffff0000u));
-                    const uint32_t l23 = pack_bf16(z[2] - __uint_as_float(h23 << 16), z[3] - __uint_as_float(h23 & 0xffff0000u));
-                    ph[t][0] = transpose8x8(h01);
-                    ph[t][1] = transpose8x8(h23);
-                    pl[t][0] = transpose8x8(l01);
-                    pl[t][1] = transpose8x8(l23);
+#pragma unroll
+                    for (int f = 0; f < 2; ++f)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = z[f][2 * e], y = z[f][2 * e + 1];
+                            const uint32_t hi = pack_bf16(x, y);
+                            const uint32_t lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+                            ph[t][f][e] = transpose8x8(hi);
+                            pl[t][f][e] = transpose8x8(lo);
+                        }
                 }
                 if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -374,33 +469,36 @@ __global__ void __launch_bounds__(kThreads) attend_bf16_kernel(const __grid_cons
 #pragma unroll
                             for (int e = 0; e < 4; ++e) o[t][k][e] *= corr[t][e & 1];
                 }
-                // values of slots behind the row's pairs may hold anything: 0 * NaN
-                const int c0 = (lane % 4) * 2;
-                const uint32_t keep0 = (c0 < nv ? 0xffffu : 0u) | (c0 + 1 < nv ? 0xffff0000u : 0u);
-                const uint32_t keep1 = (c0 + 8 < nv ? 0xffffu : 0u) | (c0 + 9 < nv ? 0xffff0000u : 0u);
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t a[4];
-                    ldsm_x4_t(vs + tile_offset<D>((lane & 7) + (lane >> 4) * 8, 2 * k + ((lane >> 3) & 1)), a);
-                    if (nv < kWarpPairs) {
-                        a[0] &= keep0;
-                        a[1] &= keep0;
-                        a[2] &= keep1;
-                        a[3] &= keep1;
-                    }
+                for (int f = 0; f < 2; ++f) {
+                    // values of slots behind the row's pairs may hold anything: 0 * NaN
+                    const int nv = note.pairs[f];
+                    const uint32_t keep0 = (c0 < nv ? 0xffffu : 0u) | (c0 + 1 < nv ? 0xffff0000u : 0u);
+                    const uint32_t keep1 = (c0 + 8 < nv ? 0xffffu : 0u) | (c0 + 9 < nv ? 0xffff0000u : 0u);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        mma16816(o[t][k], a, ph[t][0], ph[t][1]);
-                        mma16816(o[t][k], a, pl[t][0], pl[t][1]);
+                    for (int k = 0; k < KS; ++k) {
+                        uint32_t a[4];
+                        ldsm_x4_t(vs + f * HALF + L::at(v_lane, k), a);
+                        if (ragged) {
+                            a[0] &= keep0;
+                            a[1] &= keep0;
+                            a[2] &= keep1;
+                            a[3] &= keep1;
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            mma16816(o[t][k], a, ph[t][f][0], ph[t][f][1]);
+                            mma16816(o[t][k], a, pl[t][f][0], pl[t][f][1]);
+                        }
                     }
                 }
             }
             __syncwarp();
-            if (!dead) issue(st);
-            st = st + 1 == S::STAGES ? 0 : st + 1;
-            const int item0 = cur.item, row0 = cur.b;
-            cur.next(p, per_row);
-            more = cur.left > 0 && cur.item == item0 && cur.b == row0;
+            if (lane == 0) mbar_arrive(&s_free[st]);
+            if (++st == S::STAGES) {
+                st = 0;
+                parity ^= 1u;
+            }
         }
         // ---- the warps' results, joined ----------------------------------------------
 #pragma unroll
@@ -416,14 +514,14 @@ __global__ void __launch_bounds__(kThreads) attend_bf16_kernel(const __grid_cons
                     s_l[warp][t * 8 + lane * 2 + e] = x;
                 }
             }
-        __syncthreads();
+        warps_sync();
         // each warp scales its outputs to the common maximum; pairs of warps add
         float f[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int hh = t * 8 + (lane % 4) * 2 + e;
+                const int hh = t * 8 + c0 + e;
                 float mx = fmaxf(fmaxf(s_m[0][hh], s_m[1][hh]), fmaxf(s_m[2][hh], s_m[3][hh]));
                 if (mx == -INFINITY) mx = 0.f;
                 f[t][e] = ex2(m[t][e] - mx);
@@ -438,12 +536,12 @@ __global__ void __launch_bounds__(kThreads) attend_bf16_kernel(const __grid_cons
                     for (int k = 0; k < KS; ++k)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            float *x = so + (t * 8 + (lane % 4) * 2 + (e & 1)) * S::OS + k * 16 + lane / 4 + (e >> 1) * 8;
+                            float *x = so + (t * 8 + c0 + (e & 1)) * S::OS + k * 16 + r0 + (e >> 1) * 8;
                             const float val = o[t][k][e] * f[t][e & 1];
                             *x = pass == 0 ? val : *x + val;
                         }
             }
-            __syncthreads();
+            warps_sync();
         }
         float *part = p.part + (blockIdx.x + item) * part_floats(S::HEADS, D);
         for (int x = tid; x < heads * D; x += kThreads) {
@@ -458,12 +556,9 @@ __global__ void __launch_bounds__(kThreads) attend_bf16_kernel(const __grid_cons
             part[S::HEADS * D + 2 * tid] = mx;
             part[S::HEADS * D + 2 * tid + 1] = ls;
         }
-        __syncthreads();
+        warps_sync();
+        more = cur.next(p, per_row);
     }
-    // after a wait that ran out: no copy may land once the block is gone
-    if (dead)
-        for (int s = 0; s < S::STAGES; ++s)
-            if ((valid >> (8 * s)) & 0xff) mbar_wait_drain(&s_bar[warp][s], (phase >> s) & 1u);
 }
 
 // ---- float32 ----------------------------------------------------------------------
@@ -482,13 +577,14 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
     griddep_launch_dependents();
     const int per_row = p.c.H * p.items;
     Cursor cur;
-    if (!find_part(p, per_row, cur)) return;
+    if (!find_part<kWarps>(p, per_row, cur)) return;
     const float scale = rsqrtf((float)D) * 1.4426950408889634f;
     const float *kpool = reinterpret_cast<const float *>(p.c.k), *vpool = reinterpret_cast<const float *>(p.c.v);
-    while (cur.left > 0) {
-        const int b = cur.b, h = cur.item / p.items, grp = cur.item % p.items;
+    bool more = true;
+    while (more) {
+        const int b = cur.b, h = cur.item / p.items, grp = cur.item - h * p.items;
         const int h0 = h * p.G + grp * GT, heads = min(GT, p.G - grp * GT);
-        const int64_t n = cur.n, item = (int64_t)b * per_row + cur.item;
+        const int64_t item = (int64_t)b * per_row + cur.item;
         float4 q[GT], o[GT];
         float m[GT], l[GT];
 #pragma unroll
@@ -499,29 +595,29 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
             m[g] = -INFINITY;
             l[g] = 0.f;
         }
-        bool more = true;
-        while (more) {
-            const int64_t j0 = (int64_t)cur.tile * kTile + warp * kWarpPairs;
-            int nv = (int)max((int64_t)0, min((int64_t)kWarpPairs, n - j0));
+        // the warp's 32 pairs of each tile, as two runs of 16 within a page
+        for (int i2 = 0; i2 < 2 * cur.count; ++i2) {
+            const int j0 = (cur.tile + i2 / 2) * kTile + warp * kWarpPairs + (i2 & 1) * kBox;
+            int nv = max(0, min(kBox, cur.n - j0));
             int64_t row = 0;
             if (nv) {
-                const int pg = p.c.table[(int64_t)b * p.c.max_pages + j0 / p.c.page];
+                const int pi = p.c.page_of(j0), pg = p.c.table[(int64_t)b * p.c.max_pages + pi];
                 if (page_ok(p.c, pg)) {
-                    row = pool_row(p.c, pg, h, (int)(j0 % p.c.page));
+                    row = pool_row(p.c, pg, h, j0 - pi * p.c.page);
                 } else {
                     nv = 0;
                     if (lane == 0) report(p.c.status, TC_ERR_DEVICE_BOUNDS);
                 }
             }
 #pragma unroll
-            for (int u = 0; u < kWarpPairs / KPW; u += BATCH) {
+            for (int u = 0; u < kBox / KPW; u += BATCH) {
                 if (u * KPW >= nv) break;
                 float4 k4[BATCH], v4[BATCH];
 #pragma unroll
                 for (int i = 0; i < BATCH; ++i) {
                     const int j = (u + i) * KPW + sub;
                     k4[i] = v4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (u + i < kWarpPairs / KPW && j < nv) {
+                    if (u + i < kBox / KPW && j < nv) {
                         k4[i] = reinterpret_cast<const float4 *>(kpool)[(row + j) * LPK + li];
                         v4[i] = reinterpret_cast<const float4 *>(vpool)[(row + j) * LPK + li];
                     }
@@ -538,7 +634,7 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
 #pragma unroll
                         for (int off = LPK / 2; off >= 1; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
                         const int j = (u + i) * KPW + sub;
-                        const bool in = u + i < kWarpPairs / KPW && j < nv;
+                        const bool in = u + i < kBox / KPW && j < nv;
                         z[i] = x * scale;
                         if (p.z && in && li == 0 && g < heads) p.z[(row + j) * p.G + grp * GT + g] = z[i];
                         if (!in) z[i] = -INFINITY;
@@ -562,9 +658,6 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
                     }
                 }
             }
-            const int item0 = cur.item, row0 = cur.b;
-            cur.next(p, per_row);
-            more = cur.left > 0 && cur.item == item0 && cur.b == row0;
         }
 #pragma unroll
         for (int g = 0; g < GT; ++g) {
@@ -596,10 +689,14 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
             part[GT * D + 2 * tid + 1] = sum;
         }
         __syncthreads();
+        more = cur.next(p, per_row);
     }
 }
 
 // ---- the join ---------------------------------------------------------------------
+
+constexpr int kMassTiles = 16;    // tiles of a chunk of the weights
+constexpr int kMassStats = 512;   // (tile, query head) statistics of a chunk
 
 struct JoinShape {
     int y_blocks, unit_heads, units_per_bh;  // outputs: blocks, query heads a unit covers
@@ -607,28 +704,45 @@ struct JoinShape {
     int split_grid;                          // blocks of the first kernel
 };
 
-// The blocks of the first kernel that met units u0 .. u1-1 (u1 > u0).
-struct Parts {
-    int64_t first, last;
-    __device__ __forceinline__ Parts(int64_t u0, int64_t u1, int64_t total, int64_t G)
-        : first(((u0 + 1) * G - 1) / total), last((u1 * G - 1) / total) {}
-};
-
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_constant__ AttendParams p,
+__global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __grid_constant__ AttendParams p,
                                                                    const __grid_constant__ JoinShape js) {
-    constexpr int HB = 4;                    // query heads per pass over A
+    constexpr int HB = 4;                     // query heads of a batch
     constexpr int CG = D / 4, RG = kJoinThreads / CG;
-    constexpr int DG = kJoinThreads / D;     // groups of threads over the partials
+    constexpr int CHUNK = 64;                 // partials whose factors are held at a time
+    constexpr int OUT = (HB * D + kJoinThreads - 1) / kJoinThreads;  // outputs per thread
     __shared__ __align__(16) float s_red[RG][HB][D];
-    __shared__ float s_q[HB][D];
-    __shared__ float s_w[128], s_x[128];
-    __shared__ int s_row;
-    float *red = &s_red[0][0][0];
+    constexpr int WU = 4;                     // pairs per thread in flight (weights)
+    __shared__ float s_q[HB][D], s_f[HB][CHUNK], s_m[kMassStats], s_l[kMassStats];
+    __shared__ int s_b[kMassTiles], s_h[kMassTiles], s_t[kMassTiles];
+    __shared__ int s_row[kMassTiles * (kTile / kBox)], s_nv[kMassTiles * (kTile / kBox)];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const CacheParams &c = p.c;
     const int per_row = c.H * p.items;
     const int64_t pf = part_floats(p.heads, D);
+
+    // the softmax's maximum and the reciprocal of its sum, joined over np
+    // partials of one item, head hh of it; one warp
+    auto join_ml = [&](const float *part, int np, int hh, float &M, float &L) {
+        M = -INFINITY;
+        L = 0.f;
+        const float *ml = part + p.heads * D + 2 * hh;
+        for (int i = lane; i < np; i += 32) {
+            const float2 x = *reinterpret_cast<const float2 *>(ml + i * pf);
+            const float mx = fmaxf(M, x.x), ref = mx == -INFINITY ? 0.f : mx;
+            L = fmaf(L, ex2(M - ref), x.y * ex2(x.x - ref));
+            M = mx;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
+            const float mx = fmaxf(M, m2), ref = mx == -INFINITY ? 0.f : mx;
+            L = L * ex2(M - ref) + l2 * ex2(m2 - ref);
+            M = mx;
+        }
+        if (M == -INFINITY) M = 0.f;
+        L = L == 0.f ? 0.f : 1.f / L;
+    };
 
     if ((int)blockIdx.x < js.y_blocks) {
         // ---- outputs: a unit is some query heads of one (row, key/value head) --------
@@ -645,9 +759,9 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
             for (int g0 = g_begin; g0 < g_end && live; g0 += HB) {
                 const int ng = min(HB, g_end - g0);
                 const int64_t qh = (int64_t)b * p.Hq + h * p.G + g0;
-                float mem[HB * D / kJoinThreads > 0 ? HB * D / kJoinThreads : 1];  // q A of this thread's outputs
+                float mem[OUT];  // q A of this thread's outputs, tid + x kJoinThreads
 #pragma unroll
-                for (int x = 0; x < (int)(sizeof(mem) / 4); ++x) mem[x] = 0.f;
+                for (int x = 0; x < OUT; ++x) mem[x] = 0.f;
                 if (p.g && !p.memo) {
                     __syncthreads();
                     for (int x = tid; x < ng * D; x += kJoinThreads)
@@ -674,7 +788,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
                     for (int g = 0; g < HB; ++g) reinterpret_cast<float4 *>(&s_red[rg][g][0])[cg] = acc[g];
                     __syncthreads();
 #pragma unroll
-                    for (int x = 0; x < (int)(sizeof(mem) / 4); ++x) {
+                    for (int x = 0; x < OUT; ++x) {
                         const int i = tid + x * kJoinThreads;
                         if (i < ng * D)
                             for (int r = 0; r < RG; ++r) mem[x] += s_red[r][i / D][i % D];
@@ -686,53 +800,66 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
                 }
                 if (p.memo) {
 #pragma unroll
-                    for (int x = 0; x < (int)(sizeof(mem) / 4); ++x) {
+                    for (int x = 0; x < OUT; ++x) {
                         const int i = tid + x * kJoinThreads;
                         if (i < ng * D)
-                            for (int r = 0; r < p.slices; ++r)
-                                mem[x] += p.memo[((bh * p.slices + r) * p.G + g0) * D + i];
+                            for (int r = 0; r < p.slices; ++r) mem[x] += p.memo[((bh * p.slices + r) * p.G + g0) * D + i];
                     }
                 }
-                const int64_t tiles = (held + kTile - 1) / kTile;
-                const int64_t total = p.prefix[c.B] * per_row;
-                const int64_t G = total < js.split_grid ? total : js.split_grid;
-                for (int g = 0; g < ng; ++g) {
-                    const int grp = (g0 + g) / p.heads, hh = (g0 + g) % p.heads;
-                    const int64_t item = (int64_t)b * per_row + h * p.items + grp;
-                    float sum = 0.f, L = 0.f;
-                    const int d = tid % D, dg = tid / D;
-                    if (tiles > 0) {
-                        const int64_t u0 = p.prefix[b] * per_row + ((int64_t)h * p.items + grp) * tiles;
-                        const Parts ps(u0, u0 + tiles, total, G);
-                        const int64_t np = ps.last - ps.first + 1;
-                        float M = -INFINITY;
-                        for (int64_t i = 0; i < np; ++i) M = fmaxf(M, p.part[(ps.first + i + item) * pf + p.heads * D + 2 * hh]);
-                        if (M == -INFINITY) M = 0.f;
-                        for (int64_t i = dg; i < np; i += DG) {
-                            const float *part = p.part + (ps.first + i + item) * pf;
-                            const float w = ex2(part[p.heads * D + 2 * hh] - M);
-                            sum = fmaf(w, part[hh * D + d], sum);
-                            L = fmaf(w, part[p.heads * D + 2 * hh + 1], L);
+                const int tiles = (int)((held + kTile - 1) / kTile);
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                // every thread one float4 of one head, as many partials side by side as fit
+                const int width = ng * CG, groups = kJoinThreads / width;
+                const int e = tid % width, eg = e / CG, pg = tid / width;
+                if (tiles > 0) {
+                    const Cut cut((uint32_t)p.prefix[c.B] * per_row, js.split_grid);
+                    const int grp = g0 / p.heads, hh = g0 % p.heads;  // a batch never crosses a group
+                    const uint32_t u0 = (uint32_t)p.prefix[b] * per_row + (h * p.items + grp) * tiles;
+                    const int p0 = (int)cut.block_of(u0), np = (int)cut.block_of(u0 + tiles - 1) - p0 + 1;
+                    const float *part = p.part + (p0 + (int64_t)b * per_row + h * p.items + grp) * pf;
+                    __syncthreads();
+                    if (warp < ng) {
+                        float M, L;
+                        join_ml(part, np, hh + warp, M, L);
+                        if (lane == 0) {
+                            s_m[warp] = M;
+                            s_l[warp] = L;
                         }
                     }
-                    __syncthreads();
-                    red[tid] = sum;  // [DG][D]
-                    if (d == 0) s_w[dg] = L;
-                    __syncthreads();
-                    // outputs of head g belong to threads of index i = g D + d
-#pragma unroll
-                    for (int x = 0; x < (int)(sizeof(mem) / 4); ++x) {
-                        const int i = tid + x * kJoinThreads;
-                        if (i / D == g) {
-                            float num = 0.f, den = 0.f;
-                            for (int r = 0; r < DG; ++r) {
-                                num += red[r * D + i % D];
-                                den += s_w[r];
-                            }
-                            float y = den == 0.f ? 0.f : num / den;  // no pair, or none that counts
-                            if (p.g) y = fmaf(sigmoidf_acc(p.g[h * p.G + g0 + g]), mem[x], y);
-                            reinterpret_cast<T *>(p.y)[qh * D + i] = from_f32<T>(y);
+                    for (int i0 = 0; i0 < np; i0 += CHUNK) {
+                        const int nc = min(CHUNK, np - i0);
+                        __syncthreads();
+                        for (int x = tid; x < HB * CHUNK; x += kJoinThreads) {
+                            const int g = x / CHUNK, i = x % CHUNK;
+                            if (g < ng && i < nc)
+                                s_f[g][i] = ex2(part[(i0 + i) * pf + p.heads * D + 2 * (hh + g)] - s_m[g]) * s_l[g];
                         }
+                        __syncthreads();
+                        if (pg < groups) {
+#pragma unroll 4
+                            for (int i = pg; i < nc; i += groups) {
+                                const float4 o = reinterpret_cast<const float4 *>(part + (i0 + i) * pf + hh * D)[e];
+                                const float f = s_f[eg][i];
+                                acc.x = fmaf(f, o.x, acc.x);
+                                acc.y = fmaf(f, o.y, acc.y);
+                                acc.z = fmaf(f, o.z, acc.z);
+                                acc.w = fmaf(f, o.w, acc.w);
+                            }
+                        }
+                    }
+                }
+                __syncthreads();
+                float *red = &s_red[0][0][0];  // [groups][ng D]
+                if (pg < groups) reinterpret_cast<float4 *>(red)[tid] = acc;
+                __syncthreads();
+#pragma unroll
+                for (int x = 0; x < OUT; ++x) {
+                    const int i = tid + x * kJoinThreads;
+                    if (i < ng * D) {
+                        float y = 0.f;
+                        for (int r = 0; r < groups; ++r) y += red[r * ng * D + i];
+                        if (p.g) y = fmaf(sigmoidf_acc(p.g[h * p.G + g0 + i / D]), mem[x], y);
+                        reinterpret_cast<T *>(p.y)[qh * D + i] = from_f32<T>(y);
                     }
                 }
                 __syncthreads();
@@ -740,8 +867,8 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
         }
         if (!waited) griddep_wait();
         if (p.step && blockIdx.x == 0) {
-            // the step's rows, once every kernel that reads them by the old
-            // values is done: len is no longer read (row_len stands for it)
+            // the step's rows: lengths and clocks, which the step's first kernel
+            // read and nothing after it does (row_len stands for them)
             for (int b = tid; b < c.B; b += kJoinThreads)
                 if (p.row_len[b] >= 0) {
                     c.len[b] = p.row_len[b];
@@ -752,64 +879,132 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
     }
 
     // ---- weights: this block's share of the tiles of every (row, key/value head) -----
+    // A chunk of tiles at a time: which (row, head) each belongs to, the
+    // joined maximum and sum of every query head of each, then the pairs, WU per
+    // thread in flight.
     griddep_wait();
-    const int64_t mb = blockIdx.x - js.y_blocks, all = p.prefix[c.B] * c.H;
-    const int64_t total = p.prefix[c.B] * per_row;
-    const int64_t G = total < js.split_grid ? total : js.split_grid;
-    int64_t u = mb * all / js.mass_blocks;
-    const int64_t u_end = (mb + 1) * all / js.mass_blocks;
-    if (u >= u_end) return;
-    if (tid == 0) {
-        int lo = 0, hi = c.B - 1;  // the last row that begins at or before u
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (p.prefix[mid] * c.H <= u) lo = mid;
-            else hi = mid - 1;
-        }
-        s_row = lo;
-    }
-    __syncthreads();
-    int b = s_row;
+    int *s_pre = reinterpret_cast<int *>(&s_red[0][0][0]);  // rows' prefix, where it fits
+    const uint32_t all = (uint32_t)p.prefix[c.B];
+    const Cut cut(all * per_row, js.split_grid), mine(all * c.H, js.mass_blocks);
+    const uint32_t mb = blockIdx.x - js.y_blocks;
+    if (mb >= mine.G) return;
+    int u = (int)mine.begin(mb);
+    const int u_end = (int)mine.begin(mb + 1);
+    const bool fits = c.B < (int)(sizeof(s_red) / 4);
+    if (fits)
+        for (int b = tid; b <= c.B; b += kJoinThreads) s_pre[b] = p.prefix[b];
+    const int *pre = fits ? s_pre : p.prefix;
+    const int most = min(kMassTiles, kMassStats / p.G);  // tiles of a chunk: each may be another (row, head)
     while (u < u_end) {
-        while (p.prefix[b + 1] * c.H <= u) ++b;
-        const int64_t tiles = p.prefix[b + 1] - p.prefix[b], off = u - p.prefix[b] * c.H;
-        const int h = (int)(off / tiles);
-        const int64_t tile = off % tiles, stop = min(tiles, tile + (u_end - u));
-        const int64_t held = row_pairs(p, b);
-        // the softmax's maximum and sum of every head of the group, joined
+        const int nt = min(most, u_end - u);
         __syncthreads();
-        for (int g = warp; g < p.G; g += kJoinThreads / 32) {
-            const int grp = g / p.heads, hh = g % p.heads;
-            const int64_t item = (int64_t)b * per_row + h * p.items + grp;
-            const int64_t u0 = p.prefix[b] * per_row + ((int64_t)h * p.items + grp) * tiles;
-            const Parts ps(u0, u0 + tiles, total, G);
+        if (tid < nt) {
+            const int x = u + tid;
+            int lo = 0, hi = c.B - 1;  // the last row that begins at or before x
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (pre[mid] * c.H <= x) lo = mid;
+                else hi = mid - 1;
+            }
+            const int tiles = pre[lo + 1] - pre[lo], off = x - pre[lo] * c.H;
+            s_b[tid] = lo;
+            s_h[tid] = off / tiles;
+            s_t[tid] = off - s_h[tid] * tiles;
+        }
+        __syncthreads();
+        // pool row and pairs of every run of 16
+        for (int x = tid; x < nt * (kTile / kBox); x += kJoinThreads) {
+            const int i = x / (kTile / kBox), b = s_b[i], j = s_t[i] * kTile + x % (kTile / kBox) * kBox;
+            int nv = max(0, min(kBox, (int)row_pairs(p, b) - j)), row = 0;
+            if (nv) {
+                const int pi = c.page_of(j), pg = c.table[(int64_t)b * c.max_pages + pi];
+                if (page_ok(c, pg)) row = (pg * c.H + s_h[i]) * c.page + j - pi * c.page;
+                else nv = 0;
+            }
+            s_row[x] = row;
+            s_nv[x] = nv;
+        }
+        // eight lanes per (tile, query head); tiles of one (row, head) share their first tile's
+        for (int x0 = 0; x0 < nt * p.G; x0 += kJoinThreads / 8) {
+            const int x = x0 + tid / 8, l8 = tid % 8;
+            const int i = x < nt * p.G ? x / p.G : 0, g = x - i * p.G, b = s_b[i], h = s_h[i];
+            const bool lead = x < nt * p.G && (i == 0 || s_t[i] == 0);
             float M = -INFINITY, L = 0.f;
-            for (int64_t i = ps.first + lane; i <= ps.last; i += 32) M = fmaxf(M, p.part[(i + item) * pf + p.heads * D + 2 * hh]);
-#pragma unroll
-            for (int o = 16; o > 0; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            if (M == -INFINITY) M = 0.f;
-            for (int64_t i = ps.first + lane; i <= ps.last; i += 32) {
-                const float *ml = p.part + (i + item) * pf + p.heads * D + 2 * hh;
-                L = fmaf(ex2(ml[0] - M), ml[1], L);
+            if (lead) {
+                const int tiles = pre[b + 1] - pre[b], grp = g / p.heads, hh = g - grp * p.heads;
+                const uint32_t u0 = (uint32_t)pre[b] * per_row + (h * p.items + grp) * tiles;
+                const int p0 = (int)cut.block_of(u0), np = (int)cut.block_of(u0 + tiles - 1) - p0 + 1;
+                const float *ml = p.part + (p0 + (int64_t)b * per_row + h * p.items + grp) * pf + p.heads * D + 2 * hh;
+#pragma unroll 4
+                for (int k = l8; k < np; k += 8) {
+                    const float2 v = *reinterpret_cast<const float2 *>(ml + k * pf);
+                    const float mx = fmaxf(M, v.x), ref = mx == -INFINITY ? 0.f : mx;
+                    L = fmaf(L, ex2(M - ref), v.y * ex2(v.x - ref));
+                    M = mx;
+                }
             }
 #pragma unroll
-            for (int o = 16; o > 0; o /= 2) L += __shfl_xor_sync(0xffffffffu, L, o);
-            if (lane == 0) {
-                s_w[g] = M;
-                s_x[g] = L == 0.f ? 0.f : 1.f / L;
+            for (int o = 4; o > 0; o /= 2) {
+                const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
+                const float mx = fmaxf(M, m2), ref = mx == -INFINITY ? 0.f : mx;
+                L = L * ex2(M - ref) + l2 * ex2(m2 - ref);
+                M = mx;
+            }
+            if (lead && l8 == 0) {
+                s_m[x] = M == -INFINITY ? 0.f : M;
+                s_l[x] = L == 0.f ? 0.f : 1.f / L;
             }
         }
         __syncthreads();
-        const int64_t j_end = min(held, stop * kTile);
-        for (int64_t j = tile * kTile + tid; j < j_end; j += kJoinThreads) {
-            const int pg = c.table[(int64_t)b * c.max_pages + j / c.page];
-            if (!page_ok(c, pg)) continue;
-            const int64_t row = pool_row(c, pg, h, (int)(j % c.page));
-            float w = 0.f;
-            for (int g = 0; g < p.G; ++g) w = fmaf(ex2(p.z[row * p.G + g] - s_w[g]), s_x[g], w);
-            c.mass[row] += w;
+        for (int j0 = tid; j0 < nt * kTile; j0 += WU * kJoinThreads) {
+            int row[WU], stat[WU];
+#pragma unroll
+            for (int k = 0; k < WU; ++k) {
+                const int x = j0 + k * kJoinThreads, i = x / kTile, q = x / kBox;
+                row[k] = -1;
+                if (i < nt) {
+                    stat[k] = (i - min(i, s_t[i])) * p.G;  // the (row, head)'s first tile of the chunk
+                    if (x % kBox < s_nv[q]) row[k] = s_row[q] + x % kBox;
+                }
+            }
+            float w[WU], old[WU];
+#pragma unroll
+            for (int k = 0; k < WU; ++k) {
+                w[k] = 0.f;
+                if (row[k] >= 0) old[k] = c.mass[row[k]];
+            }
+            if (p.G % 4 == 0) {
+                for (int g = 0; g < p.G; g += 4) {
+                    float4 z[WU];
+#pragma unroll
+                    for (int k = 0; k < WU; ++k)
+                        if (row[k] >= 0) z[k] = *reinterpret_cast<const float4 *>(p.z + (int64_t)row[k] * p.G + g);
+#pragma unroll
+                    for (int k = 0; k < WU; ++k)
+                        if (row[k] >= 0) {
+                            const int s = stat[k] + g;
+                            w[k] = fmaf(ex2(z[k].x - s_m[s]), s_l[s], w[k]);
+                            w[k] = fmaf(ex2(z[k].y - s_m[s + 1]), s_l[s + 1], w[k]);
+                            w[k] = fmaf(ex2(z[k].z - s_m[s + 2]), s_l[s + 2], w[k]);
+                            w[k] = fmaf(ex2(z[k].w - s_m[s + 3]), s_l[s + 3], w[k]);
+                        }
+                }
+            } else {
+                for (int g = 0; g < p.G; ++g) {
+                    float z[WU];
+#pragma unroll
+                    for (int k = 0; k < WU; ++k)
+                        if (row[k] >= 0) z[k] = p.z[(int64_t)row[k] * p.G + g];
+#pragma unroll
+                    for (int k = 0; k < WU; ++k)
+                        if (row[k] >= 0) w[k] = fmaf(ex2(z[k] - s_m[stat[k] + g]), s_l[stat[k] + g], w[k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < WU; ++k)
+                if (row[k] >= 0) c.mass[row[k]] = old[k] + w[k];
         }
-        u += stop - tile;
+        u += nt;
     }
 }
 
@@ -819,13 +1014,13 @@ typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, 
                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The pool as rows of d bf16; boxes of 16 rows, at most 64 columns.
-bool make_pool_map(CUtensorMap *m, const void *base, int64_t rows, int d) {
+// The pool as rows of d bf16; boxes of at most 64 columns.
+bool make_pool_map(CUtensorMap *m, const void *base, int64_t rows, int d, int box_rows) {
     EncodeTiled fn = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)(d < 64 ? d : 64), (cuuint32_t)kWarpPairs};
+    const cuuint32_t box[2] = {(cuuint32_t)(d < 64 ? d : 64), (cuuint32_t)box_rows};
     const cuuint32_t es[2] = {1, 1};
     const CUtensorMapSwizzle sw = d >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : d == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
@@ -835,11 +1030,11 @@ bool make_pool_map(CUtensorMap *m, const void *base, int64_t rows, int d) {
 
 // Resident blocks of a kernel over the device, at most attend_grid's bound.
 template <typename K>
-cudaError_t fill_grid(K kernel, int smem, int num_sms, int *grid) {
+cudaError_t fill_grid(K kernel, int threads, int smem, int num_sms, int *grid) {
     cudaError_t e = smem > 0 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
     if (e != cudaSuccess) return e;
     int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
     if (e != cudaSuccess) return e;
     const int most = attend_grid(num_sms);
     *grid = per_sm * num_sms < most ? per_sm * num_sms : most;
@@ -863,17 +1058,20 @@ template <int D, int NT>
 cudaError_t split_bf16(const AttendParams &p, int num_sms, int *grid, cudaStream_t s) {
     CUtensorMap mk, mv;
     const int64_t rows = (int64_t)p.c.n_pages * p.c.H * p.c.page;
-    if (!make_pool_map(&mk, p.c.k, rows, D) || !make_pool_map(&mv, p.c.v, rows, D)) return cudaErrorInvalidValue;
-    cudaError_t e = fill_grid(attend_bf16_kernel<D, NT>, Bf16Shape<D, NT>::SMEM, num_sms, grid);
+    // a warp's 32 pairs are in one page, or in two halves that may be in two
+    const int box_rows = p.c.page % kWarpPairs == 0 ? kWarpPairs : kBox;
+    if (!make_pool_map(&mk, p.c.k, rows, D, box_rows) || !make_pool_map(&mv, p.c.v, rows, D, box_rows))
+        return cudaErrorInvalidValue;
+    cudaError_t e = fill_grid(attend_bf16_kernel<D, NT>, kThreads + 32, Bf16Shape<D, NT>::SMEM, num_sms, grid);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = early_launch(&attr, *grid, kThreads, Bf16Shape<D, NT>::SMEM, s, p.step);
-    return cudaLaunchKernelEx(&cfg, attend_bf16_kernel<D, NT>, mk, mv, p);
+    const cudaLaunchConfig_t cfg = early_launch(&attr, *grid, kThreads + 32, Bf16Shape<D, NT>::SMEM, s, p.step);
+    return cudaLaunchKernelEx(&cfg, attend_bf16_kernel<D, NT>, mk, mv, p, box_rows);
 }
 
 template <int D, int GT>
 cudaError_t split_f32(const AttendParams &p, int num_sms, int *grid, cudaStream_t s) {
-    cudaError_t e = fill_grid(attend_f32_kernel<D, GT>, 0, num_sms, grid);
+    cudaError_t e = fill_grid(attend_f32_kernel<D, GT>, kThreads, 0, num_sms, grid);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = early_launch(&attr, *grid, kThreads, 0, s, p.step);
@@ -904,7 +1102,7 @@ cudaError_t launch_attend_d(const AttendParams &p, tc_dtype dtype, int num_sms, 
     js.units_per_bh = (p.G + js.unit_heads - 1) / js.unit_heads;
     const int64_t units = BH * js.units_per_bh;
     js.y_blocks = (int)(units < 8 * num_sms ? units : 8 * num_sms);
-    js.mass_blocks = p.z ? 2 * num_sms : 0;
+    js.mass_blocks = p.z ? 4 * num_sms : 0;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = early_launch(&attr, js.y_blocks + js.mass_blocks, kJoinThreads, 0, s, true);
     return dtype == TC_BF16 ? cudaLaunchKernelEx(&cfg, attend_join_kernel<__nv_bfloat16, D>, p, js)
@@ -927,6 +1125,8 @@ size_t attend_part_bytes(int64_t BH, int G, int d, tc_dtype dtype, int num_sms) 
     const int64_t items = BH * ((G + heads - 1) / heads);
     return (size_t)(attend_grid(num_sms) + items) * (size_t)part_floats(heads, d) * sizeof(float);
 }
+
+double attend_units(double items, int64_t capacity) { return items * (double)((capacity + kTile - 1) / kTile); }
 
 bool attend_supported(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 

@@ -10,14 +10,15 @@
 // leave in that order, and
 //   A <- lambda^m A + eta sum_i lambda^(m-1-i) k_i v_i^T.
 // One cluster owns one (row, head); each of its blocks finds the same pairs on
-// its own (no exchange) and writes its own slice of A's rows.  m = 1, the
-// steady state, is an arg-min over the weights beside one pass over A, which is
-// what bounds it: 8 d^2 bytes of A, plus 8 n of weights and positions.  m > 1
-// sorts the weights in shared memory and forms the sum tile by tile.
-
-#include <cooperative_groups.h>
+// its own (no exchange) and writes its own slice of A's rows.  Rows of which
+// one pair leaves (the steady state: an arg-min over the weights beside one
+// pass over A, 8 d^2 bytes of A and 8 n of weights and positions) are the first
+// kernel's; the second takes the rest (a sort, and products on the tensor
+// cores) and stores the new lengths, which the first has to leave for its other
+// blocks to read.
 
 #include "paged_cache.cuh"
+#include "sm100_ptx.cuh"
 
 namespace tc {
 namespace {
@@ -131,12 +132,6 @@ cudaError_t launch_append_vec(const AppendParams &p, cudaStream_t s) {
 
 // ---- eviction -------------------------------------------------------------------
 
-constexpr int kEvThreads = 256;
-constexpr int kEvWarps = kEvThreads / 32;
-constexpr int kSortMax = 8192;   // pairs sorted in shared memory (12 bytes each)
-constexpr int kPairTile = 32;    // pairs per step of the weighted sum
-constexpr int kQBatch = 4;       // query heads per pass over A's registers
-
 // The order in which pairs leave, as one number: unprotected first, then by
 // weight (NaN last, -0 as 0), then by position.
 __device__ __forceinline__ uint64_t leave_key(float mass, int32_t pos, int64_t protect_from) {
@@ -145,6 +140,276 @@ __device__ __forceinline__ uint64_t leave_key(float mass, int32_t pos, int64_t p
     if (mass != mass) u = 0xffffffffu;
     return ((uint64_t)(pos >= protect_from) << 63) | ((uint64_t)u << 31) | (uint32_t)(pos & 0x7fffffff);
 }
+__device__ __forceinline__ bool less_pair(uint64_t ka, uint32_t sa, uint64_t kb, uint32_t sb) {
+    return ka < kb || (ka == kb && sa < sb);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The row's pairs before the call's eviction (a step's new pair among them), or
+// -1 for a row that is skipped (*bad: and reported).  Block-wide.
+__device__ __forceinline__ int64_t evict_pairs(const EvictParams &p, bool step, int b, int64_t clock, bool &bad) {
+    const int64_t held = p.c.len[b], n = held + (step ? 1 : 0);
+    bad = false;
+    if (held < 0) return -1;
+    bad = held > p.c.capacity() || n > p.c.capacity() || (step && (clock < 0 || clock >= (int64_t(1) << 31)));
+    if (!bad) bad = !block_pages_ok(p.c, b, 0, n - 1);
+    return bad ? -1 : n;
+}
+
+// ---- at most one pair leaves (the steady state; the step's first kernel) ----------
+//
+// The slice of A comes in by one bulk copy while the weights are looked
+// through, so it holds no registers; with d^2 / slices floats a block (32 KB at
+// most) several blocks share an SM and cover one another's latencies, of which
+// the chain length -> table -> weights -> pair -> A has many.
+constexpr int kOneThreads = 256;
+constexpr int kOneWarps = kOneThreads / 32;
+constexpr int kQBatch = 4;    // query heads per pass over A
+constexpr int kScanBatch = 4; // weights in flight per thread
+
+template <typename T, int D, bool STEP>
+__global__ void __launch_bounds__(kOneThreads) evict_one_kernel(const __grid_constant__ EvictParams p, int slices) {
+    constexpr int CG = D / 4;              // float4 columns of A
+    constexpr int RG = kOneThreads / CG;   // rows of A side by side
+    extern __shared__ __align__(128) unsigned char dyn[];
+    __shared__ __align__(16) float s_k[D], s_v[D];
+    __shared__ float s_cos[D / 2 + 1], s_sin[D / 2 + 1];
+    __shared__ uint64_t s_key[kOneWarps];
+    __shared__ uint32_t s_slot[kOneWarps];
+    __shared__ float s_q[kQBatch][D];
+    __shared__ __align__(16) float s_mp[RG][kQBatch][D];
+    __shared__ __align__(8) uint64_t s_bar;
+    __shared__ int s_abort;
+
+    const CacheParams &c = p.c;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = blockIdx.x % slices;
+    const int64_t bh = blockIdx.x / slices;
+    const int b = (int)(bh / c.H), h = (int)(bh % c.H);
+    const int64_t clock0 = c.clock[b];
+    const bool first = h == 0 && rank == 0 && tid == 0;
+    const int rows = D / slices, row0 = rank * rows;
+    const bool read = STEP && p.memo != nullptr;
+    float4 *A4 = c.A ? reinterpret_cast<float4 *>(c.A + (bh * D + row0) * D) : nullptr;
+    float4 *sA = reinterpret_cast<float4 *>(dyn);
+    const int64_t expect = c.len[b] + (STEP ? 1 : 0);
+    const bool copy = A4 && expect >= 0 && (read || expect > p.budget) && (STEP || expect - p.budget == 1);
+    if (tid == 0) {
+        s_abort = 0;
+        sm100::mbar_init(&s_bar, 1);
+        sm100::fence_mbar_init();
+        if (copy) {
+            sm100::mbar_expect_tx(&s_bar, (uint32_t)(rows * D * 4));
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             sm100::smem_u32(dyn)),
+                         "l"(A4), "r"(rows * D * 4), "r"(sm100::smem_u32(&s_bar))
+                         : "memory");
+        }
+    }
+    bool bad;
+    const int64_t n64 = evict_pairs(p, STEP, b, clock0, bad);  // its barrier also publishes s_bar
+    // a step lets one pair leave at most: a row above its budget stays above
+    const int64_t over = n64 - p.budget;
+    const int m = over <= 0 ? 0 : STEP ? 1 : over == 1 ? 1 : 0;
+    const int n = (int)n64, keep = n - m;
+    if (first) {
+        if (bad) report(c.status, TC_ERR_DEVICE_BOUNDS);
+        p.row_len[b] = n64 < 0 ? -1 : STEP ? keep : n64;
+    }
+    if (n64 < 0 || (m == 0 && !STEP)) {
+        if (copy && tid == 0) sm100::mbar_wait_drain(&s_bar, 0);
+        return;  // the whole cluster
+    }
+    const int32_t *table = c.table + (int64_t)b * c.max_pages;
+    auto row_of = [&](int slot) {
+        const int pg = c.page_of(slot);
+        return pool_row(c, table[pg], h, slot - pg * c.page);
+    };
+    T *kp = reinterpret_cast<T *>(c.k), *vp = reinterpret_cast<T *>(c.v);
+    const int G = STEP ? p.Hq / c.H : 0;
+
+    if (STEP) {
+        // the new pair enters slot n - 1 (every block of the cluster writes the
+        // same values), the queries are rotated
+        const RotaryTable &rt = p.table;
+        for (int i = tid; i < rt.rot / 2; i += kOneThreads) rotary_angle(clock0, rt.inc[i], rt.gain, s_cos[i], s_sin[i]);
+        __syncthreads();
+        const int64_t row = row_of(n - 1);
+        for (int x = tid; x < (G + 2) * D; x += kOneThreads) {
+            const int which = x / D, i = x % D;
+            if (which == G + 1) {
+                vp[row * D + i] = reinterpret_cast<const T *>(p.v_new)[b * p.vs[0] + h * p.vs[1] + i];
+                continue;
+            }
+            const T *src = which == G ? reinterpret_cast<const T *>(p.k_new) + b * p.ks[0] + h * p.ks[1]
+                                      : reinterpret_cast<const T *>(p.q) + b * p.qs[0] + (h * G + which) * p.qs[1];
+            float f = to_f32(src[i]);
+            if (i < rt.rot) {
+                const int half = rt.rot / 2;
+                const int pair = rt.interleaved ? i / 2 : i < half ? i : i - half;
+                const bool second = rt.interleaved ? (i & 1) : i >= half;
+                const int other = rt.interleaved ? i ^ 1 : (second ? i - half : i + half);
+                const float g = to_f32(src[other]);
+                f = second ? g * s_sin[pair] + f * s_cos[pair] : f * s_cos[pair] - g * s_sin[pair];
+            }
+            if (which == G) kp[row * D + i] = from_f32<T>(f);
+            else reinterpret_cast<T *>(p.q_rot)[(bh * G + which) * D + i] = from_f32<T>(f);
+        }
+        if (tid == 0) {
+            c.mass[row] = 0.f;
+            c.pos[row] = (int32_t)clock0;
+        }
+        __syncthreads();
+    }
+
+    int gone = 0;  // the slot that leaves
+    if (m == 1) {
+        const int64_t protect_from = clock0 + (STEP ? 1 : 0) - p.recent;
+        uint64_t best = ~0ull;
+        uint32_t slot = 0xffffffffu;
+        for (int s0 = tid; s0 < n; s0 += kScanBatch * kOneThreads) {
+            float w[kScanBatch];
+            int32_t z[kScanBatch];
+#pragma unroll
+            for (int i = 0; i < kScanBatch; ++i) {
+                const int s = s0 + i * kOneThreads;
+                if (s < n) {
+                    const int64_t row = row_of(s);
+                    w[i] = c.mass[row];
+                    z[i] = c.pos[row];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kScanBatch; ++i) {
+                const int s = s0 + i * kOneThreads;
+                if (s < n) {
+                    const uint64_t key = leave_key(w[i], z[i], protect_from);
+                    if (less_pair(key, (uint32_t)s, best, slot)) {
+                        best = key;
+                        slot = (uint32_t)s;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) {
+            const uint64_t k2 = __shfl_xor_sync(0xffffffffu, best, o);
+            const uint32_t s2 = __shfl_xor_sync(0xffffffffu, slot, o);
+            if (less_pair(k2, s2, best, slot)) {
+                best = k2;
+                slot = s2;
+            }
+        }
+        if (lane == 0) {
+            s_key[warp] = best;
+            s_slot[warp] = slot;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kOneWarps; ++w)
+            if (w == 0 || less_pair(s_key[w], s_slot[w], best, slot)) {
+                best = s_key[w];
+                slot = s_slot[w];
+            }
+        gone = (int)slot;
+    }
+
+    if (copy) {
+        const int cg = tid % CG, rg = tid / CG;
+        const float lam = c.lam[h], eta = c.eta[h];
+        if (m == 1) {
+            const int64_t row = row_of(gone);
+            for (int i = tid; i < 2 * D; i += kOneThreads) {
+                if (i < D) s_k[i] = to_f32(kp[row * D + i]);
+                else s_v[i - D] = to_f32(vp[row * D + i - D]);
+            }
+        }
+        if (!sm100::mbar_wait(&s_bar, 0, &s_abort, c.status, p.wait_ns)) sm100::mbar_wait_drain(&s_bar, 0);
+        __syncthreads();
+        const float4 v4 = m == 1 ? reinterpret_cast<const float4 *>(s_v)[cg] : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int g0 = 0; g0 == 0 || g0 < G; g0 += kQBatch) {
+            const int ng = read ? min(kQBatch, G - g0) : 0;
+            if (read) {
+                for (int x = tid; x < kQBatch * rows; x += kOneThreads) {
+                    const int g = x / rows, r = x - g * rows;
+                    s_q[g][r] = g < ng ? to_f32(reinterpret_cast<const T *>(p.q_rot)[(bh * G + g0 + g) * D + row0 + r]) : 0.f;
+                }
+                __syncthreads();
+            }
+            float4 mp[kQBatch];
+#pragma unroll
+            for (int g = 0; g < kQBatch; ++g) mp[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int r = rg; r < rows; r += RG) {
+                float4 a = sA[r * CG + cg];
+                if (g0 == 0 && m == 1) {
+                    const float ek = eta * s_k[row0 + r];
+                    a.x = fmaf(lam, a.x, ek * v4.x);
+                    a.y = fmaf(lam, a.y, ek * v4.y);
+                    a.z = fmaf(lam, a.z, ek * v4.z);
+                    a.w = fmaf(lam, a.w, ek * v4.w);
+                    A4[r * CG + cg] = a;
+                    if (G > kQBatch) sA[r * CG + cg] = a;
+                }
+                if (read) {
+#pragma unroll
+                    for (int g = 0; g < kQBatch; ++g) {
+                        const float w = s_q[g][r];
+                        mp[g].x = fmaf(w, a.x, mp[g].x);
+                        mp[g].y = fmaf(w, a.y, mp[g].y);
+                        mp[g].z = fmaf(w, a.z, mp[g].z);
+                        mp[g].w = fmaf(w, a.w, mp[g].w);
+                    }
+                }
+            }
+            if (read) {
+#pragma unroll
+                for (int g = 0; g < kQBatch; ++g) reinterpret_cast<float4 *>(&s_mp[rg][g][0])[cg] = mp[g];
+                __syncthreads();
+                for (int x = tid; x < ng * D; x += kOneThreads) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int r = 0; r < RG; ++r) sum += s_mp[r][x / D][x % D];
+                    p.memo[((bh * slices + rank) * G + g0) * D + x] = sum;
+                }
+                __syncthreads();
+            }
+        }
+    }
+    if (m == 0) return;  // the whole cluster
+
+    // the last pair moves to the freed slot, once every block of the cluster has
+    // read what that overwrites
+    if (slices > 1) cluster_sync();
+    else __syncthreads();
+    constexpr int LPR = D * (int)sizeof(T) / 16;  // 16-byte vectors of a row
+    if (rank == 0 && gone < keep && tid < 2 * LPR) {
+        const int64_t from = row_of(keep), to = row_of(gone);
+        T *pool = tid < LPR ? kp : vp;
+        const int i = tid < LPR ? tid : tid - LPR;
+        reinterpret_cast<uint4 *>(pool + to * D)[i] = reinterpret_cast<const uint4 *>(pool + from * D)[i];
+        if (tid == 0) {
+            c.mass[to] = c.mass[from];
+            c.pos[to] = c.pos[from];
+        }
+    }
+}
+
+// ---- several pairs leave ------------------------------------------------------------
+//
+// The pairs are sorted by leave_key (bitonic, in shared memory up to kSortMax),
+// and the weighted sum runs on the tensor cores: tiles of TP pairs come in by
+// asynchronous 16-byte copies, double buffered; the weighted keys
+// lambda^(m-1-i) k_i are split into three bf16 parts (24 bits together; a
+// float32 cache's values too), and the products' sums over one tile are added
+// to float32 sums with the ordinary rounding, because the tensor cores' own
+// accumulation truncates and would drift over thousands of pairs.
+constexpr int kBulkThreads = 512;
+constexpr int kBulkWarps = kBulkThreads / 32;
+constexpr int kSortMax = 8192;   // pairs sorted in shared memory (12 bytes each)
 
 // lambda^j for j >= 0 to float32's precision: the exponent in 64 bits, its
 // fraction to exp2f.
@@ -163,16 +428,12 @@ struct Decay {
     }
 };
 
-__device__ __forceinline__ bool less_pair(uint64_t ka, uint32_t sa, uint64_t kb, uint32_t sb) {
-    return ka < kb || (ka == kb && sa < sb);
-}
-
 // Bitonic sort of n2 (a power of two) keys with their slots, ascending.
 __device__ void block_sort(uint64_t *key, uint32_t *slot, int n2) {
     for (int size = 2; size <= n2; size *= 2) {
         for (int stride = size / 2; stride > 0; stride /= 2) {
             __syncthreads();
-            for (int i = threadIdx.x; i < n2 / 2; i += kEvThreads) {
+            for (int i = threadIdx.x; i < n2 / 2; i += kBulkThreads) {
                 const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
                 const bool up = (lo & size) == 0;
                 const uint64_t ka = key[lo], kb = key[hi];
@@ -203,7 +464,7 @@ __device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < kEvWarps; ++w) {
+    for (int w = 0; w < kBulkWarps; ++w) {
         if (w < warp) before += warp_sums[w];
         all += warp_sums[w];
     }
@@ -211,363 +472,361 @@ __device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
     return before + v - x;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void ldsm_t4(const void *p, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(sm100::smem_u32(p))
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_t2(const void *p, uint32_t (&r)[2]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+                 : "=r"(r[0]), "=r"(r[1])
+                 : "r"(sm100::smem_u32(p))
+                 : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm100::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void zero16(void *dst) { *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0); }
+
+// x, y as three bf16 pairs whose sum is exact to 24 bits.
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&o)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        o[i] = pack_bf16_rn(x, y);
+        const float hx = __uint_as_float(o[i] << 16), hy = __uint_as_float(o[i] & 0xffff0000u);
+        x = isinf(hx) ? 0.f : x - hx;  // an infinity has no rest
+        y = isinf(hy) ? 0.f : y - hy;
+    }
 }
 
-template <typename T, int D, bool STEP>
-__global__ void __launch_bounds__(kEvThreads) evict_kernel(const __grid_constant__ EvictParams p, int slices, int n2_cap) {
-    constexpr int CG = D / 4;                 // float4 columns of A
-    constexpr int RG = kEvThreads / CG;       // rows of A the block holds side by side
-    constexpr int RPT = (D + RG - 1) / RG;    // rows per thread of a whole A
-    extern __shared__ __align__(16) unsigned char dyn[];
-    __shared__ float s_k[D], s_v[D], s_cos[D / 2 + 1], s_sin[D / 2 + 1];
-    __shared__ uint64_t s_key[kEvWarps];
-    __shared__ uint32_t s_slot[kEvWarps];
-    __shared__ int s_scan[kEvWarps];
-    __shared__ float s_q[kQBatch][D];
-    __shared__ __align__(16) float s_mp[RG][kQBatch][D];
+// Shared memory of one block: raw tiles (two), the parts, sorting room.
+template <typename T, int D, int SL>
+struct BulkShape {
+    static constexpr int R = D / SL;                        // rows of A
+    static constexpr int TP = sizeof(T) == 2 ? 64 : 32;     // pairs per tile
+    static constexpr int VPARTS = sizeof(T) == 2 ? 0 : 3;   // bf16 values go in as they are
+    static constexpr int KRAW = R * (int)sizeof(T);         // bytes of a raw row
+    static constexpr int VRAW = D * (int)sizeof(T) + 16;    // padded: conflict-free reads by ldmatrix
+    static constexpr int KS = R * 2 + 16, VS = D * 2 + 16;  // bytes of a row of a part
+    static constexpr int RAW = TP * (KRAW + VRAW);
+    static constexpr int PARTS = TP * (3 * KS + VPARTS * VS);
+    static constexpr int SMEM = 2 * RAW + PARTS;            // the sorting room follows
+    // output tiles of 16 x 8: warps along the rows first
+    static constexpr int TM = R / 16, TN = D / 8, NWN = kBulkWarps / TM;
+    static constexpr int NT = TN / NWN > 0 ? TN / NWN : 1;  // tiles a warp holds
+};
+
+template <typename T, int D, int SL>
+__global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_constant__ EvictParams p, int n2_cap) {
+    using S = BulkShape<T, D, SL>;
+    extern __shared__ __align__(128) unsigned char dyn[];
+    __shared__ int s_scan[kBulkWarps];
+    __shared__ int64_t s_row[2][S::TP];
+    __shared__ float s_w[2][S::TP];
 
     const CacheParams &c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = blockIdx.x % slices;
-    const int64_t bh = blockIdx.x / slices;
+    const int rank = blockIdx.x % SL;
+    const int64_t bh = blockIdx.x / SL;
     const int b = (int)(bh / c.H), h = (int)(bh % c.H);
-    const int64_t held = c.len[b], clock0 = c.clock[b];
-    const bool first = h == 0 && rank == 0 && tid == 0;
-    if (held < 0) {
-        if (first) p.row_len[b] = -1;
-        return;
-    }
-    const int64_t n64 = held + (STEP ? 1 : 0);
-    bool ok = held <= c.capacity() && n64 <= c.capacity() &&
-              (!STEP || (clock0 >= 0 && clock0 < (int64_t(1) << 31)));
-    if (ok) ok = block_pages_ok(c, b, 0, n64 - 1);
-    if (!ok) {
-        if (first) {
-            p.row_len[b] = -1;
-            report(c.status, TC_ERR_DEVICE_BOUNDS);
-        }
-        return;
-    }
-    const int n = (int)n64;
-    const int m = n64 > p.budget ? (int)(n64 - p.budget) : 0;
-    const int keep = n - m;
-    const int64_t clock = clock0 + (STEP ? 1 : 0);
-    if (first) p.row_len[b] = keep;
+    sm100::griddep_wait();
+    const int64_t n64 = p.row_len[b];
+    if (n64 <= p.budget) return;  // empty, skipped, or nothing to do: the whole cluster
+    const int n = (int)n64, keep = (int)p.budget, m = n - keep;
+    if (h == 0 && rank == 0 && tid == 0) c.len[b] = keep;  // read by no block of this kernel
+    if (m == 1) return;
     const int32_t *table = c.table + (int64_t)b * c.max_pages;
-    auto row_of = [&](int slot) { return pool_row(c, table[slot / c.page], h, slot % c.page); };
+    auto row_of = [&](int slot) {
+        const int pg = c.page_of(slot);
+        return pool_row(c, table[pg], h, slot - pg * c.page);
+    };
     T *kp = reinterpret_cast<T *>(c.k), *vp = reinterpret_cast<T *>(c.v);
 
-    // this block's slice of A's rows, read while the weights are looked through
-    const int rows = D / slices, row0 = rank * rows;
-    const bool read = STEP && p.memo != nullptr;
-    const bool simple = m <= 1;
-    const int cg = tid % CG, rg = tid / CG;
-    float4 *A4 = c.A ? reinterpret_cast<float4 *>(c.A + (bh * D + row0) * D) : nullptr;
-    float4 a[RPT];
-    if (A4 && simple && (m == 1 || read)) {
-#pragma unroll
-        for (int i = 0; i < RPT; ++i)
-            if (rg + i * RG < rows) a[i] = A4[(rg + i * RG) * CG + cg];
-    }
-
-    if (STEP) {
-        // the new pair enters slot n - 1 (every block of the cluster writes the
-        // same values), the queries are rotated
-        const RotaryTable &rt = p.table;
-        for (int i = tid; i < rt.rot / 2; i += kEvThreads) rotary_angle(clock0, rt.inc[i], rt.gain, s_cos[i], s_sin[i]);
-        __syncthreads();
-        const int64_t row = row_of(n - 1);
-        const int G = p.Hq / c.H;
-        for (int x = tid; x < (G + 2) * D; x += kEvThreads) {
-            const int which = x / D, i = x % D;
-            if (which == G + 1) {
-                vp[row * D + i] = reinterpret_cast<const T *>(p.v_new)[b * p.vs[0] + h * p.vs[1] + i];
-                continue;
-            }
-            const T *src = which == G ? reinterpret_cast<const T *>(p.k_new) + b * p.ks[0] + h * p.ks[1]
-                                      : reinterpret_cast<const T *>(p.q) + b * p.qs[0] + (h * G + which) * p.qs[1];
-            float f = to_f32(src[i]);
-            if (i < rt.rot) {
-                const int half = rt.rot / 2;
-                const int pair = rt.interleaved ? i / 2 : i % half;
-                const bool second = rt.interleaved ? (i & 1) : i >= half;
-                const int other = rt.interleaved ? i ^ 1 : (second ? i - half : i + half);
-                const float g = to_f32(src[other]);
-                f = second ? g * s_sin[pair] + f * s_cos[pair] : f * s_cos[pair] - g * s_sin[pair];
-            }
-            if (which == G) kp[row * D + i] = from_f32<T>(f);
-            else reinterpret_cast<T *>(p.q_rot)[(bh * G + which) * D + i] = from_f32<T>(f);
-        }
-        if (tid == 0) {
-            c.mass[row] = 0.f;
-            c.pos[row] = (int32_t)clock0;
-        }
-        __syncthreads();
-    }
-    if (m == 0 && !read) return;  // the whole cluster
-
-    const int64_t protect_from = clock - p.recent;
-    const float lam = c.A ? c.lam[h] : 0.f, eta = c.A ? c.eta[h] : 0.f;
-    // lists for m > 1: the pairs that leave, in order, and the moves
-    int moves = 0;
-    int *hole = nullptr, *fill = nullptr;
-    int gone = 0;  // m == 1: the slot that leaves
-
-    if (m == 1) {
-        uint64_t best = ~0ull;
-        uint32_t slot = 0xffffffffu;
-        for (int s = tid; s < n; s += kEvThreads) {
+    // ---- the order of leaving -----------------------------------------------------
+    const int64_t protect_from = c.clock[b] - p.recent;
+    int n2 = 1;
+    while (n2 < n) n2 *= 2;
+    const bool inside = n2 <= n2_cap;
+    const int room = inside ? n2_cap : n2_cap_global(c.capacity());
+    unsigned char *ws = inside ? dyn + S::SMEM : p.sort_ws + (bh * SL + rank) * (size_t)room * 13;
+    uint64_t *key = reinterpret_cast<uint64_t *>(ws);
+    uint32_t *slot = reinterpret_cast<uint32_t *>(ws + (size_t)room * 8);
+    uint32_t *bits = reinterpret_cast<uint32_t *>(ws + (size_t)room * 12);
+    const int words = (n + 31) / 32;
+    for (int s = tid; s < n2; s += kBulkThreads) {
+        uint64_t x = ~0ull;
+        if (s < n) {
             const int64_t row = row_of(s);
-            const uint64_t key = leave_key(c.mass[row], c.pos[row], protect_from);
-            if (less_pair(key, (uint32_t)s, best, slot)) {
-                best = key;
-                slot = (uint32_t)s;
-            }
+            x = leave_key(c.mass[row], c.pos[row], protect_from);
         }
+        key[s] = x;
+        slot[s] = s < n ? (uint32_t)s : 0xffffffffu;
+    }
+    for (int s = tid; s < words; s += kBulkThreads) bits[s] = 0;
+    block_sort(key, slot, n2);
+
+    // ---- A's slice: lambda^m A + eta sum of lambda^(m-1-i) k_i v_i^T ----------------
+    if (c.A) {
+        const Decay decay(c.lam[h]);
+        const int row0 = rank * S::R;
+        unsigned char *parts = dyn + 2 * S::RAW;
+        const int wm = warp % S::TM, wn = (warp / S::TM) * S::NT;
+        const bool works = wn < S::TN;
+        float sum[S::NT][4];
 #pragma unroll
-        for (int o = 16; o > 0; o /= 2) {
-            const uint64_t k2 = __shfl_xor_sync(0xffffffffu, best, o);
-            const uint32_t s2 = __shfl_xor_sync(0xffffffffu, slot, o);
-            if (less_pair(k2, s2, best, slot)) {
-                best = k2;
-                slot = s2;
+        for (int t = 0; t < S::NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[t][e] = 0.f;
+        const int tiles = (m + S::TP - 1) / S::TP;
+        // pool rows and weights of a tile's pairs
+        auto plan = [&](int tile) {
+            if (tid < S::TP) {
+                const int i = tile * S::TP + tid;
+                s_row[tile & 1][tid] = i < m ? row_of((int)slot[i]) : -1;
+                s_w[tile & 1][tid] = i < m ? decay.pow(m - 1 - i) : 0.f;
             }
-        }
-        if (lane == 0) {
-            s_key[warp] = best;
-            s_slot[warp] = slot;
-        }
+        };
+        auto fetch = [&](int tile) {
+            unsigned char *raw = dyn + (tile & 1) * S::RAW;
+            constexpr int KC = S::KRAW / 16, VC = D * (int)sizeof(T) / 16;
+            for (int x = tid; x < S::TP * (KC + VC); x += kBulkThreads) {
+                const int pr = x / (KC + VC), ch = x % (KC + VC);
+                const int64_t row = s_row[tile & 1][pr];
+                unsigned char *dst = ch < KC ? raw + pr * S::KRAW + ch * 16 : raw + S::TP * S::KRAW + pr * S::VRAW + (ch - KC) * 16;
+                const T *src = ch < KC ? kp + row * D + row0 + ch * (16 / (int)sizeof(T)) : vp + row * D + (ch - KC) * (16 / (int)sizeof(T));
+                if (row >= 0) copy16(dst, src);
+                else zero16(dst);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        plan(0);
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kEvWarps; ++w)
-            if (w == 0 || less_pair(s_key[w], s_slot[w], best, slot)) {
-                best = s_key[w];
-                slot = s_slot[w];
-            }
-        gone = (int)slot;
-        if (A4) {
-            const int64_t row = row_of(gone);
-            for (int i = tid; i < D; i += kEvThreads) {
-                s_k[i] = to_f32(kp[row * D + i]);
-                s_v[i] = to_f32(vp[row * D + i]);
+        fetch(0);
+        if (tiles > 1) plan(1);
+        for (int tile = 0; tile < tiles; ++tile) {
+            __syncthreads();  // the next tile's plan is there, the other buffer and the parts are free
+            if (tile + 1 < tiles) {
+                fetch(tile + 1);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
             }
             __syncthreads();
-            const float4 v4 = reinterpret_cast<const float4 *>(s_v)[cg];
+            const unsigned char *raw = dyn + (tile & 1) * S::RAW;
+            for (int x = tid; x < S::TP * S::R / 2; x += kBulkThreads) {
+                const int pr = x / (S::R / 2), e = x % (S::R / 2);
+                const T *src = reinterpret_cast<const T *>(raw + pr * S::KRAW) + 2 * e;
+                const float w = s_w[tile & 1][pr];
+                uint32_t o[3];
+                split3(w * to_f32(src[0]), w * to_f32(src[1]), o);
 #pragma unroll
-            for (int i = 0; i < RPT; ++i) {
-                const int r = rg + i * RG;
-                if (r < rows) {
-                    const float ek = eta * s_k[row0 + r];
-                    a[i].x = fmaf(lam, a[i].x, ek * v4.x);
-                    a[i].y = fmaf(lam, a[i].y, ek * v4.y);
-                    a[i].z = fmaf(lam, a[i].z, ek * v4.z);
-                    a[i].w = fmaf(lam, a[i].w, ek * v4.w);
-                    A4[r * CG + cg] = a[i];
+                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(parts + i * S::TP * S::KS + pr * S::KS + e * 4) = o[i];
+            }
+            if (S::VPARTS) {
+                for (int x = tid; x < S::TP * D / 2; x += kBulkThreads) {
+                    const int pr = x / (D / 2), e = x % (D / 2);
+                    const T *src = reinterpret_cast<const T *>(raw + S::TP * S::KRAW + pr * S::VRAW) + 2 * e;
+                    uint32_t o[3];
+                    split3(to_f32(src[0]), to_f32(src[1]), o);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        *reinterpret_cast<uint32_t *>(parts + 3 * S::TP * S::KS + i * S::TP * S::VS + pr * S::VS + e * 4) = o[i];
                 }
             }
-        }
-    } else if (m > 1) {
-        // ---- the order of leaving ------------------------------------------------
-        int n2 = 1;
-        while (n2 < n) n2 *= 2;
-        unsigned char *ws = n2 <= n2_cap ? dyn : p.sort_ws + bh * ((size_t)n2_cap_global(c.capacity()) * 13);
-        const int n2_room = n2 <= n2_cap ? n2_cap : n2_cap_global(c.capacity());
-        uint64_t *key = reinterpret_cast<uint64_t *>(ws);
-        uint32_t *slot = reinterpret_cast<uint32_t *>(ws + (size_t)n2_room * 8);
-        uint32_t *bits = reinterpret_cast<uint32_t *>(ws + (size_t)n2_room * 12);
-        const int words = (n + 31) / 32;
-        for (int s = tid; s < n2; s += kEvThreads) {
-            uint64_t x = ~0ull;
-            if (s < n) {
-                const int64_t row = row_of(s);
-                x = leave_key(c.mass[row], c.pos[row], protect_from);
-            }
-            key[s] = x;
-            slot[s] = s < n ? (uint32_t)s : 0xffffffffu;
-        }
-        for (int s = tid; s < words; s += kEvThreads) bits[s] = 0;
-        block_sort(key, slot, n2);
-
-        // ---- A's slice: lambda^m A + eta sum of lambda^(m-1-i) k_i v_i^T ----------
-        if (A4) {
-            const Decay decay(lam);
-            float *tk = reinterpret_cast<float *>(dyn + (size_t)n2_cap * 13);  // [kPairTile][rows] weighted keys
-            float *tv = tk + kPairTile * rows;                                 // [kPairTile][D]
-            float4 acc[RPT];
+            __syncthreads();
+            if (tile + 2 < tiles) plan(tile + 2);
+            if (works) {
+                const unsigned char *vbase = S::VPARTS ? parts + 3 * S::TP * S::KS : raw + S::TP * S::KRAW;
+                constexpr int VROW = S::VPARTS ? S::VS : S::VRAW;
+                float acc[S::NT][4];
 #pragma unroll
-            for (int i = 0; i < RPT; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i0 = 0; i0 < m; i0 += kPairTile) {
-                const int np = min(kPairTile, m - i0);
-                __syncthreads();
-                for (int x = tid; x < np * (rows + D); x += kEvThreads) {
-                    const int pr = x / (rows + D), e = x % (rows + D);
-                    const int64_t row = row_of((int)slot[i0 + pr]);
-                    if (e < rows)
-                        tk[pr * rows + e] = eta * decay.pow(m - 1 - (i0 + pr)) * to_f32(kp[row * D + row0 + e]);
-                    else
-                        tv[pr * D + e - rows] = to_f32(vp[row * D + e - rows]);
-                }
-                __syncthreads();
-                for (int pr = 0; pr < np; ++pr) {
-                    const float4 v4 = reinterpret_cast<const float4 *>(tv + pr * D)[cg];
+                for (int t = 0; t < S::NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < RPT; ++i) {
-                        const int r = rg + i * RG;
-                        if (r < rows) {
-                            const float w = tk[pr * rows + r];
-                            acc[i].x = fmaf(w, v4.x, acc[i].x);
-                            acc[i].y = fmaf(w, v4.y, acc[i].y);
-                            acc[i].z = fmaf(w, v4.z, acc[i].z);
-                            acc[i].w = fmaf(w, v4.w, acc[i].w);
+                    for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < S::TP / 16; ++k) {
+                    // keys [pair][row]: as the transposed operand, pairs along k
+                    uint32_t a[3][4];
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        ldsm_t4(parts + i * S::TP * S::KS + (k * 16 + (lane & 7) + (lane >> 4) * 8) * S::KS + (wm * 16 + ((lane >> 3) & 1) * 8) * 2, a[i]);
+#pragma unroll
+                    for (int t = 0; t < S::NT; ++t) {
+#pragma unroll
+                        for (int j = 0; j < (S::VPARTS ? 3 : 1); ++j) {
+                            uint32_t v[2];
+                            ldsm_t2(vbase + j * S::TP * S::VS + (k * 16 + (lane & 15)) * VROW + (wn + t) * 16, v);
+#pragma unroll
+                            for (int i = 2 - j; i >= 0; --i) mma_bf16(acc[t], a[i], v);
                         }
                     }
                 }
-            }
-            const float lm = decay.pow(m);
 #pragma unroll
-            for (int i = 0; i < RPT; ++i) {
-                const int r = rg + i * RG;
-                if (r < rows) {
-                    const float4 o = A4[r * CG + cg];
-                    a[i].x = fmaf(lm, o.x, acc[i].x);
-                    a[i].y = fmaf(lm, o.y, acc[i].y);
-                    a[i].z = fmaf(lm, o.z, acc[i].z);
-                    a[i].w = fmaf(lm, o.w, acc[i].w);
-                    A4[r * CG + cg] = a[i];
-                }
+                for (int t = 0; t < S::NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[t][e] += acc[t][e];
             }
         }
-
-        // ---- freed slots below keep, and the pairs behind it that stay ------------
-        for (int i = tid; i < m; i += kEvThreads) atomicOr(&bits[slot[i] / 32], 1u << (slot[i] % 32));
-        __syncthreads();  // the keys are done with: their room takes the two lists
-        hole = reinterpret_cast<int *>(key);
-        fill = hole + n2_room;
-        const int per = (words + kEvThreads - 1) / kEvThreads;
-        auto freed = [&](int w) {  // slots of word w that leave and are below keep
-            const int below = keep - w * 32;
-            return below <= 0 ? 0u : bits[w] & (below >= 32 ? ~0u : (1u << below) - 1u);
-        };
-        auto stays = [&](int w) {  // slots of word w at or behind keep, held, that stay
-            const int below = keep - w * 32, end = n - w * 32;
-            uint32_t x = ~bits[w];
-            if (below >= 32) return 0u;
-            if (below > 0) x &= ~((1u << below) - 1u);
-            if (end < 32) x &= (1u << end) - 1u;
-            return x;
-        };
-        int nh = 0, nf = 0, total;
-        for (int w = tid * per; w < min(words, (tid + 1) * per); ++w) {
-            nh += __popc(freed(w));
-            nf += __popc(stays(w));
+        if (works) {
+            const float lm = decay.pow(m), eta = c.eta[h];
+#pragma unroll
+            for (int t = 0; t < S::NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    float2 *x = reinterpret_cast<float2 *>(c.A + (bh * D + row0 + wm * 16 + lane / 4 + e * 4) * D + (wn + t) * 8 + (lane % 4) * 2);
+                    float2 o = *x;
+                    o.x = fmaf(lm, o.x, eta * sum[t][e]);
+                    o.y = fmaf(lm, o.y, eta * sum[t][e + 1]);
+                    *x = o;
+                }
         }
-        int ih = block_scan(nh, s_scan, &moves);
-        int jf = block_scan(nf, s_scan, &total);
-        for (int w = tid * per; w < min(words, (tid + 1) * per); ++w) {
-            for (uint32_t x = freed(w); x; x &= x - 1) hole[ih++] = w * 32 + __ffs(x) - 1;
-            for (uint32_t x = stays(w); x; x &= x - 1) fill[jf++] = w * 32 + __ffs(x) - 1;
-        }
-        __syncthreads();
     }
 
-    // ---- q A for the step's queries, from the slice of A just written -------------
-    if (read) {
-        const int G = p.Hq / c.H;
-        for (int g0 = 0; g0 < G; g0 += kQBatch) {
-            const int ng = min(kQBatch, G - g0);
-            __syncthreads();
-            for (int x = tid; x < ng * rows; x += kEvThreads)
-                s_q[x / rows][x % rows] = to_f32(reinterpret_cast<const T *>(p.q_rot)[(bh * G + g0 + x / rows) * D + row0 + x % rows]);
-            __syncthreads();
-#pragma unroll
-            for (int g = 0; g < kQBatch; ++g) {
-                float4 mp = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < RPT; ++i) {
-                    const int r = rg + i * RG;
-                    if (r < rows) {
-                        const float w = g < ng ? s_q[g][r] : 0.f;
-                        mp.x = fmaf(w, a[i].x, mp.x);
-                        mp.y = fmaf(w, a[i].y, mp.y);
-                        mp.z = fmaf(w, a[i].z, mp.z);
-                        mp.w = fmaf(w, a[i].w, mp.w);
-                    }
-                }
-                reinterpret_cast<float4 *>(&s_mp[rg][g][0])[cg] = mp;
-            }
-            __syncthreads();
-            for (int x = tid; x < ng * D; x += kEvThreads) {
-                float sum = 0.f;
-#pragma unroll
-                for (int r = 0; r < RG; ++r) sum += s_mp[r][x / D][x % D];
-                p.memo[((bh * slices + rank) * G + g0) * D + x] = sum;
-            }
-        }
+    // ---- freed slots below keep, and the pairs behind it that stay ------------------
+    for (int i = tid; i < m; i += kBulkThreads) atomicOr(&bits[slot[i] / 32], 1u << (slot[i] % 32));
+    __syncthreads();  // the keys are done with: their room takes the two lists
+    int *hole = reinterpret_cast<int *>(key), *fill = hole + room;
+    const int per = (words + kBulkThreads - 1) / kBulkThreads;
+    auto freed = [&](int w) {  // slots of word w that leave and are below keep
+        const int below = keep - w * 32;
+        return below <= 0 ? 0u : bits[w] & (below >= 32 ? ~0u : (1u << below) - 1u);
+    };
+    auto stays = [&](int w) {  // slots of word w at or behind keep, held, that stay
+        const int below = keep - w * 32, end = n - w * 32;
+        uint32_t x = ~bits[w];
+        if (below >= 32) return 0u;
+        if (below > 0) x &= ~((1u << below) - 1u);
+        if (end < 32) x &= (1u << end) - 1u;
+        return x;
+    };
+    int nh = 0, nf = 0, moves, total;
+    for (int w = tid * per; w < min(words, (tid + 1) * per); ++w) {
+        nh += __popc(freed(w));
+        nf += __popc(stays(w));
     }
-    if (m == 0) return;  // the whole cluster
+    int ih = block_scan(nh, s_scan, &moves);
+    int jf = block_scan(nf, s_scan, &total);
+    for (int w = tid * per; w < min(words, (tid + 1) * per); ++w) {
+        for (uint32_t x = freed(w); x; x &= x - 1) hole[ih++] = (int)row_of(w * 32 + __ffs(x) - 1);
+        for (uint32_t x = stays(w); x; x &= x - 1) fill[jf++] = (int)row_of(w * 32 + __ffs(x) - 1);
+    }
 
-    // ---- moves, once every block of the cluster has read what they overwrite ------
-    if (slices > 1) cluster_sync();
+    // ---- moves, once every block of the cluster has read what they overwrite --------
+    if (SL > 1) cluster_sync();
     else __syncthreads();
-    if (m == 1) moves = gone < keep ? 1 : 0;
     constexpr int LPR = D * (int)sizeof(T) / 16;  // 16-byte vectors of a row
-    for (int x = rank * kEvWarps + warp; x < moves; x += slices * kEvWarps) {
-        const int64_t from = row_of(m == 1 ? keep : fill[x]), to = row_of(m == 1 ? gone : hole[x]);
-        const uint4 *ks = reinterpret_cast<const uint4 *>(kp + from * D), *vs = reinterpret_cast<const uint4 *>(vp + from * D);
-        uint4 *kd = reinterpret_cast<uint4 *>(kp + to * D), *vd = reinterpret_cast<uint4 *>(vp + to * D);
-        for (int i = lane; i < 2 * LPR; i += 32) {
-            if (i < LPR) kd[i] = ks[i];
-            else vd[i - LPR] = vs[i - LPR];
+    constexpr int UN = 4;                         // vectors in flight per thread
+    const int64_t vectors = (int64_t)moves * 2 * LPR;
+    for (int64_t x0 = (int64_t)rank * kBulkThreads + tid; x0 < vectors; x0 += (int64_t)UN * SL * kBulkThreads) {
+        uint4 val[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int64_t x = x0 + (int64_t)u * SL * kBulkThreads;
+            if (x < vectors) {
+                const int mv = (int)(x / (2 * LPR)), i = (int)(x % (2 * LPR));
+                const T *pool = i < LPR ? kp : vp;
+                val[u] = reinterpret_cast<const uint4 *>(pool + (int64_t)fill[mv] * D)[i < LPR ? i : i - LPR];
+            }
         }
-        if (lane == 0) {
-            c.mass[to] = c.mass[from];
-            c.pos[to] = c.pos[from];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int64_t x = x0 + (int64_t)u * SL * kBulkThreads;
+            if (x < vectors) {
+                const int mv = (int)(x / (2 * LPR)), i = (int)(x % (2 * LPR));
+                T *pool = i < LPR ? kp : vp;
+                reinterpret_cast<uint4 *>(pool + (int64_t)hole[mv] * D)[i < LPR ? i : i - LPR] = val[u];
+            }
         }
+    }
+    for (int x = rank * kBulkThreads + tid; x < moves; x += SL * kBulkThreads) {
+        c.mass[hole[x]] = c.mass[fill[x]];
+        c.pos[hole[x]] = c.pos[fill[x]];
     }
 }
 
-__global__ void evict_finish_kernel(int64_t *len, const int64_t *row_len, int B) {
-    const int b = blockIdx.x * blockDim.x + threadIdx.x;
-    if (b < B && row_len[b] >= 0) len[b] = row_len[b];
-}
-
-size_t evict_smem(int n2, int d, int slices) {
-    return (size_t)n2 * 13 + (size_t)kPairTile * (d / slices + d) * sizeof(float);
-}
-
-template <typename T, int D, bool STEP>
-cudaError_t launch_evict_t(const EvictParams &p, int slices, cudaStream_t s) {
-    const int64_t cap = n2_cap_global(p.c.capacity());
-    const int n2 = (int)(cap < kSortMax ? cap : kSortMax);
-    const size_t smem = evict_smem(n2, D, slices);
-    cudaError_t e = cudaFuncSetAttribute(evict_kernel<T, D, STEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
+cudaLaunchConfig_t cluster_launch(cudaLaunchAttribute *attr, int64_t grid, int threads, size_t smem, int slices, bool early, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)slices;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)p.c.B * p.c.H * slices));
-    cfg.blockDim = dim3(kEvThreads);
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_kernel<T, D, STEP>, p, slices, n2);
+    cfg.numAttrs = early ? 2 : 1;
+    return cfg;
+}
+
+template <typename T, int D, bool STEP>
+cudaError_t launch_one(const EvictParams &p, int slices, cudaStream_t s) {
+    const size_t smem = p.c.A ? (size_t)D * D / slices * sizeof(float) : 0;
+    cudaError_t e = allow_smem(evict_one_kernel<T, D, STEP>, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = cluster_launch(attr, (int64_t)p.c.B * p.c.H * slices, kOneThreads, smem, slices, false, s);
+    return cudaLaunchKernelEx(&cfg, evict_one_kernel<T, D, STEP>, p, slices);
+}
+
+template <typename T, int D, int SL>
+cudaError_t launch_bulk(const EvictParams &p, cudaStream_t s) {
+    const int64_t cap = n2_cap_global(p.c.capacity());
+    const int n2 = (int)(cap < kSortMax ? cap : kSortMax);
+    const size_t smem = BulkShape<T, D, SL>::SMEM + (size_t)n2 * 13;
+    cudaError_t e = allow_smem(evict_bulk_kernel<T, D, SL>, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = cluster_launch(attr, (int64_t)p.c.B * p.c.H * SL, kBulkThreads, smem, SL, true, s);
+    return cudaLaunchKernelEx(&cfg, evict_bulk_kernel<T, D, SL>, p, n2);
+}
+
+template <typename T, int D>
+cudaError_t launch_bulk_sl(const EvictParams &p, int slices, cudaStream_t s) {
+    if constexpr (D >= 64)
+        if (slices == 4) return launch_bulk<T, D, 4>(p, s);
+    if constexpr (D >= 32)
+        if (slices == 2) return launch_bulk<T, D, 2>(p, s);
+    return launch_bulk<T, D, 1>(p, s);
+}
+
+template <typename T>
+cudaError_t launch_bulk_d(const EvictParams &p, int d, int slices, cudaStream_t s) {
+    switch (d) {
+        case 16: return launch_bulk_sl<T, 16>(p, slices, s);
+        case 32: return launch_bulk_sl<T, 32>(p, slices, s);
+        case 64: return launch_bulk_sl<T, 64>(p, slices, s);
+        case 128: return launch_bulk_sl<T, 128>(p, slices, s);
+    }
+    return cudaErrorInvalidValue;
 }
 
 template <typename T, bool STEP>
-cudaError_t launch_evict_d(const EvictParams &p, int d, int slices, cudaStream_t s) {
+cudaError_t launch_one_d(const EvictParams &p, int d, int slices, cudaStream_t s) {
     switch (d) {
-        case 16: return launch_evict_t<T, 16, STEP>(p, slices, s);
-        case 32: return launch_evict_t<T, 32, STEP>(p, slices, s);
-        case 64: return launch_evict_t<T, 64, STEP>(p, slices, s);
-        case 128: return launch_evict_t<T, 128, STEP>(p, slices, s);
+        case 16: return launch_one<T, 16, STEP>(p, slices, s);
+        case 32: return launch_one<T, 32, STEP>(p, slices, s);
+        case 64: return launch_one<T, 64, STEP>(p, slices, s);
+        case 128: return launch_one<T, 128, STEP>(p, slices, s);
     }
     return cudaErrorInvalidValue;
+}
+
+// Slices a head's A is cut into, one block of a cluster each, of 16 rows at
+// least: more while the device has room for them, `least` at any rate.
+int slices_for(int64_t BH, int d, int least, int most, int num_sms) {
+    int slices = least;
+    while (slices * 2 <= d / 16 && slices < most && BH * slices * 2 <= 2 * num_sms) slices *= 2;
+    return slices;
 }
 
 }  // namespace
@@ -584,29 +843,28 @@ cudaError_t launch_cache_append(const AppendParams &p, tc_dtype dtype, cudaStrea
     return wide ? launch_append_vec<float, 4>(p, s) : launch_append_vec<float, 1>(p, s);
 }
 
-// A slice has at least 16 rows of A; rows that sort in global memory stay whole
-// (their workspace is per head).
-int evict_slices(int64_t BH, int d, int64_t capacity, int num_sms) {
-    int slices = 1;
-    if (n2_cap_global(capacity) > kSortMax) return 1;
-    while (slices * 2 <= d / 16 && slices < 8 && BH * slices * 2 <= 2 * num_sms) slices *= 2;
-    return slices;
-}
+// 32 KB of A a block at most, so that several share an SM.
+int evict_slices(int64_t BH, int d, int num_sms) { return slices_for(BH, d, d == 128 ? 2 : 1, 4, num_sms); }
 
-size_t evict_sort_bytes(int64_t BH, int64_t capacity) {
+namespace {
+int bulk_slices(int64_t BH, int d, int num_sms) { return slices_for(BH, d, 1, 4, num_sms); }
+}  // namespace
+
+size_t evict_sort_bytes(int64_t BH, int d, int64_t capacity, int num_sms) {
     const int64_t n2 = n2_cap_global(capacity);
-    return n2 <= kSortMax ? 0 : (size_t)BH * (size_t)n2 * 13;
+    return n2 <= kSortMax ? 0 : (size_t)BH * (size_t)bulk_slices(BH, d, num_sms) * (size_t)n2 * 13;
 }
 
-cudaError_t launch_cache_evict(const EvictParams &p, tc_dtype dtype, int d, bool step, int slices, cudaStream_t s) {
-    if (dtype == TC_BF16)
-        return step ? launch_evict_d<__nv_bfloat16, true>(p, d, slices, s) : launch_evict_d<__nv_bfloat16, false>(p, d, slices, s);
-    return step ? launch_evict_d<float, true>(p, d, slices, s) : launch_evict_d<float, false>(p, d, slices, s);
+cudaError_t launch_cache_step_insert(const EvictParams &p, tc_dtype dtype, int d, int slices, cudaStream_t s) {
+    return dtype == TC_BF16 ? launch_one_d<__nv_bfloat16, true>(p, d, slices, s) : launch_one_d<float, true>(p, d, slices, s);
 }
 
-cudaError_t launch_cache_evict_finish(const EvictParams &p, cudaStream_t s) {
-    evict_finish_kernel<<<(p.c.B + 255) / 256, 256, 0, s>>>(p.c.len, p.row_len, p.c.B);
-    return cudaGetLastError();
+cudaError_t launch_cache_evict(const EvictParams &p, tc_dtype dtype, int d, int num_sms, cudaStream_t s) {
+    const int64_t BH = (int64_t)p.c.B * p.c.H;
+    const int one = evict_slices(BH, d, num_sms), bulk = bulk_slices(BH, d, num_sms);
+    const cudaError_t e = dtype == TC_BF16 ? launch_one_d<__nv_bfloat16, false>(p, d, one, s) : launch_one_d<float, false>(p, d, one, s);
+    if (e != cudaSuccess) return e;
+    return dtype == TC_BF16 ? launch_bulk_d<__nv_bfloat16>(p, d, bulk, s) : launch_bulk_d<float>(p, d, bulk, s);
 }
 
 }  // namespace tc

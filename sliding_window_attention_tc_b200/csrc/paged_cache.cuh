@@ -16,8 +16,10 @@ struct CacheParams {
     const float *lam, *eta;
     int B, H, page, n_pages, max_pages;
     int *status;
+    uint64_t page_mul;  // ceil(2^40 / page): slot / page = slot * page_mul >> 40 for slots below 2^24
 
     __host__ __device__ int64_t capacity() const { return (int64_t)max_pages * page; }
+    __device__ __forceinline__ int page_of(int slot) const { return (int)(((uint64_t)slot * page_mul) >> 40); }
 };
 
 // The power of two a row's pairs are sorted in: at least 32, at least capacity.
@@ -59,7 +61,8 @@ cudaError_t launch_cache_append(const AppendParams &p, tc_dtype dtype, cudaStrea
 struct EvictParams {
     CacheParams c;
     int64_t budget, recent;
-    int64_t *row_len;        // [B] what each row holds afterwards; -1: skipped
+    int64_t *row_len;        // [B] -1: skipped; a step: what the row holds afterwards;
+                             // an eviction: what it held before
     unsigned char *sort_ws;  // rows that do not fit shared memory; else null
     // tc_cache_step: the new token (one per row) and the queries
     const void *q, *k_new, *v_new;
@@ -68,13 +71,15 @@ struct EvictParams {
     float *memo;             // [B,H,slices,G,d] q A by slices of A's rows; null: no read
     int Hq;
     RotaryTable table;
+    unsigned long long wait_ns;
 };
-// Slices a head's A is cut into (one block of a cluster each): few heads get
-// more, so that the device is filled.
-int evict_slices(int64_t BH, int d, int64_t capacity, int num_sms);
-size_t evict_sort_bytes(int64_t BH, int64_t capacity);
-cudaError_t launch_cache_evict(const EvictParams &p, tc_dtype dtype, int d, bool step, int slices, cudaStream_t s);
-cudaError_t launch_cache_evict_finish(const EvictParams &p, cudaStream_t s);
+// Blocks a head's A is cut over in a step's first kernel (and p.memo's slices).
+int evict_slices(int64_t BH, int d, int num_sms);
+size_t evict_sort_bytes(int64_t BH, int d, int64_t capacity, int num_sms);
+// The new token enters, at most one pair leaves, the queries read A; lengths and
+// clocks are left to the attention's join.
+cudaError_t launch_cache_step_insert(const EvictParams &p, tc_dtype dtype, int d, int slices, cudaStream_t s);
+cudaError_t launch_cache_evict(const EvictParams &p, tc_dtype dtype, int d, int num_sms, cudaStream_t s);
 
 struct AttendParams {
     CacheParams c;
@@ -88,7 +93,7 @@ struct AttendParams {
     int Hq, G, d;
     int heads;               // query heads one work item covers
     int items;               // work items a row and key/value head has
-    int64_t *prefix;         // [B+1] tiles before each row
+    int *prefix;             // [B+1] tiles before each row
     float *part;             // partial results, one per (block, item) met
     float *z;                // scaled scores [n_pages,H,page,G]; null: weights are not kept
     unsigned long long wait_ns;
@@ -97,6 +102,17 @@ int attend_heads_per_item(int G, tc_dtype dtype);
 int attend_grid(int num_sms);
 size_t attend_part_bytes(int64_t BH, int G, int d, tc_dtype dtype, int num_sms);
 bool attend_supported(int d);
+// Units of work (tiles) at most, for the limit of 31 bits.
+double attend_units(double items, int64_t capacity);
 cudaError_t launch_cache_attend(const AttendParams &p, tc_dtype dtype, int num_sms, cudaStream_t s);
+
+// Lets a kernel use this much dynamic shared memory.  Below 16 KB it needs no
+// leave: with the static arrays (at most 32 KB) it stays within the 48 KB every
+// kernel may use.
+template <typename K>
+inline cudaError_t allow_smem(K kernel, size_t bytes) {
+    return bytes < 16 * 1024 ? cudaSuccess
+                              : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
 
 }  // namespace tc

@@ -336,7 +336,7 @@ def test_step_is_append_evict_attend(cuda_device, dtype, d, H, G, spec, memory):
     """cache_step against the three calls (the same bits in the state) and against
     the definition, over steps that cross the budget and a page's end."""
     import sliding_window_attention_tc_b200 as tc
-    held, budget, recent, steps = [20, 31, 32, 33, -1, 0, 60], 32, 3, 5
+    held, budget, recent, steps = [20, 31, 32, 17, -1, 0, 29], 32, 3, 5
     a, cpu = make(held, d=d, H=H, dtype=dtype, seed=d, memory=memory)
     b, _ = make(held, d=d, H=H, dtype=dtype, seed=d, memory=memory)
     gen = torch.Generator().manual_seed(31)
@@ -374,6 +374,40 @@ def test_step_is_append_evict_attend(cuda_device, dtype, d, H, G, spec, memory):
         check_y(y3, want, tol)
     same_state(a, cpu, A_terms=64, mass_tol=2 * steps * G * MASS_TOL)
     assert tc.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_step_many_rows(cuda_device, dtype):
+    """Enough rows that a head's A is no longer cut finer to fill the device."""
+    import sliding_window_attention_tc_b200 as tc
+    held, H, G, d, budget = [31, 20, 32, 0] * 45, 2, 2, 128, 32
+    c, cpu = make(held, d=d, H=H, dtype=dtype, seed=15, room=16)
+    gen = torch.Generator().manual_seed(16)
+    q, k, v = (torch.randn(len(held), h, d, generator=gen).to(DT[dtype]) for h in (H * G, H, H))
+    g = torch.randn(H * G, generator=gen)
+    for _ in range(2):
+        y = tc.cache_step(c, q.cuda(), k.cuda(), v.cuda(), budget, g=g.cuda())
+        cpu.append(k[:, :, None], v[:, :, None])
+        cpu.evict(budget, 1)
+        check_y(y, *cpu.attend(q, g, True))
+    same_state(c, cpu, A_terms=4, mass_tol=4 * G * MASS_TOL)
+    assert tc.device_status() == 0
+
+
+def test_step_above_the_budget_keeps_its_distance(cuda_device):
+    """A row above its budget lets one pair leave a step, the least attended one."""
+    import sliding_window_attention_tc_b200 as tc
+    c, cpu = make([50, 20], H=2, seed=12, width=6)
+    q, k, v = (torch.randn(2, h, 64).bfloat16() for h in (4, 2, 2))
+    for i in range(3):
+        tc.cache_step(c, q.cuda(), k.cuda(), v.cuda(), 32, accumulate=False)
+        cpu.append(k[:, :, None], v[:, :, None])
+        n1 = cpu.lens[1]
+        cpu.lens[1] = 0
+        cpu.evict(50, 1)
+        cpu.lens[1] = n1
+        same_state(c, cpu, A_terms=8)
+    assert c.lens.tolist() == [50, 23]
 
 
 def test_captured_step_replays(cuda_device):
