@@ -12,16 +12,19 @@
 // of each row's stretches, the memory's read, and (from the scores the first
 // kernel left in the workspace) the weights.
 //
-// bf16: each of the four warps takes 32 pairs of a tile, on its own: its own
-// place in a ring of TMA loads (boxes of 32 rows, or 16 where a page's end may fall between;
-// swizzled), brought in by a lane of a fifth warp, and its own running
-// statistics; no barrier between warps until a row's stretch ends.  Products run as S^T = K Q^T (16 pairs x 8 heads) and
+// bf16: a tile comes in by TMA (boxes of as many rows as always share a page;
+// swizzled; one lane of a ninth warp a box) and each of eight warps takes 16 of
+// its pairs, with running statistics of its own: no barrier between warps until
+// a row's stretch ends.  Products run as S^T = K Q^T (16 pairs x 8 heads) and
 // O^T = V^T P^T with m16n8k16: with the pairs as M, eight heads fill a product
 // that would be half empty with the heads as M, and the same lanes hold a
 // head's scores and its outputs, so rescaling needs no exchange.  P enters as a
 // bf16 pair hi + lo, so the outputs keep float32's precision up to their one
 // rounding.  The tensor pipe is nowhere near busy (16 d multiply-adds a pair
-// against 4 d bytes), so what matters is the loads in flight.
+// against 4 d bytes); a warp's chain score -> maximum -> weight -> output is
+// what has to be hidden, by the other warps and the loads in flight.  (Four
+// warps of 32 pairs each took 2090 cycles a tile with the data at hand, where
+// memory brings one in 2670.)
 //
 // float32: the same walk with float32 multiply-adds, d/4 lanes per pair.
 
@@ -38,36 +41,44 @@ namespace {
 using namespace sm100;
 
 constexpr int kTile = 128;       // pairs per tile
-constexpr int kWarps = 4;        // warps that compute, in the first kernel
-constexpr int kThreads = kWarps * 32;
-constexpr int kWarpPairs = 32;   // pairs of a tile one warp takes
-constexpr int kBox = 16;         // pairs that always share a page
+constexpr int kRun = 16;         // pairs that always share a page
+constexpr int kRuns = kTile / kRun;
+constexpr int kExtra = 1;        // tiles' worth of work that a row's item costs besides its tiles
 constexpr int kJoinThreads = 256;
 
 __device__ __forceinline__ int64_t row_pairs(const AttendParams &p, int b) {
     const int64_t n = p.row_len[b];
     return n < 0 || n > p.c.capacity() ? 0 : n;
 }
-__device__ __forceinline__ int row_tiles(const AttendParams &p, int b) {
-    return (int)((row_pairs(p, b) + kTile - 1) / kTile);
+// Units of work of one item of row b: its tiles and, where it has any, kExtra
+// that stand for what a stretch costs by itself (its queries, its partials).
+__device__ __forceinline__ int row_units(const AttendParams &p, int b) {
+    const int tiles = (int)((row_pairs(p, b) + kTile - 1) / kTile);
+    return tiles ? tiles + kExtra : 0;
 }
 
 // A place in the laid-out work, and the stretch of tiles from there on that
-// belongs to one (row, item): tiles .. of it are this block's.
+// belongs to one (row, item): tiles tile .. tile + count - 1 of it are this
+// block's (none when only the units that stand for no tile are).
 struct Cursor {
     int left;      // units until the end of the part, from the stretch's first
-    int b, item, tile, tiles;  // row, item of it, first tile, tiles a row's item has
+    int b, item;   // row, item of it
+    int tile, tiles;  // first tile, tiles an item of the row has
+    int units;     // of the stretch
+    int count;     // tiles of it
     int n;         // pairs of row b
-    int count;     // tiles of the stretch
 
     __device__ __forceinline__ void enter_row(const AttendParams &p) {
         n = (int)row_pairs(p, b);
         tiles = (n + kTile - 1) / kTile;
     }
-    __device__ __forceinline__ void measure() { count = min(tiles - tile, left); }
+    __device__ __forceinline__ void measure() {
+        units = min(tiles + kExtra - tile, left);
+        count = max(0, min(tiles - tile, left));
+    }
     // on to the next stretch; false at the part's end
     __device__ __forceinline__ bool next(const AttendParams &p, int per_row) {
-        left -= count;
+        left -= units;
         if (left == 0) return false;
         tile = 0;
         if (++item == per_row) {
@@ -78,6 +89,12 @@ struct Cursor {
             } while (tiles == 0);  // left > 0: a row with tiles follows
         }
         measure();
+        return true;
+    }
+    // to the first stretch that has tiles; false when the part has none
+    __device__ __forceinline__ bool settle(const AttendParams &p, int per_row) {
+        while (count == 0)
+            if (!next(p, per_row)) return false;
         return true;
     }
 };
@@ -99,8 +116,8 @@ struct Cut {
     }
 };
 
-// This block's part of the per_row * (tiles of all rows) units.  Every block
-// adds up the rows' tiles by itself; block 0 also stores them (prefix) for the
+// This block's part of the per_row * (units of all rows) units.  Every block
+// adds up the rows' units by itself; block 0 also stores them (prefix) for the
 // join.  Returns false when there is nothing to do.  Block-wide; WARPS warps.
 template <int WARPS>
 __device__ __forceinline__ bool find_part(const AttendParams &p, int per_row, Cursor &cur) {
@@ -110,7 +127,7 @@ __device__ __forceinline__ bool find_part(const AttendParams &p, int per_row, Cu
     const int per = (B + WARPS * 32 - 1) / (WARPS * 32);
     const int b0 = tid * per, b1 = min(B, b0 + per);
     int mine = 0;
-    for (int b = b0; b < b1; ++b) mine += row_tiles(p, b);
+    for (int b = b0; b < b1; ++b) mine += row_units(p, b);
     int v = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -130,7 +147,7 @@ __device__ __forceinline__ bool find_part(const AttendParams &p, int per_row, Cu
         int x = before;
         for (int b = b0; b < b1; ++b) {
             p.prefix[b] = x;
-            x += row_tiles(p, b);
+            x += row_units(p, b);
         }
         if (tid == 0) p.prefix[B] = all;
     }
@@ -140,7 +157,7 @@ __device__ __forceinline__ bool find_part(const AttendParams &p, int per_row, Cu
     if (u0 >= before * per_row && u0 < (before + mine) * per_row) {
         int x = before, b = b0;
         for (;; ++b) {
-            const int t = row_tiles(p, b);
+            const int t = row_units(p, b);
             if (u0 < (x + t) * per_row) break;
             x += t;
         }
@@ -150,11 +167,11 @@ __device__ __forceinline__ bool find_part(const AttendParams &p, int per_row, Cu
     __syncthreads();
     cur.b = s_row;
     cur.enter_row(p);
-    cur.item = s_off / cur.tiles;
-    cur.tile = s_off - cur.item * cur.tiles;
+    cur.item = s_off / (cur.tiles + kExtra);
+    cur.tile = s_off - cur.item * (cur.tiles + kExtra);
     cur.left = u1 - u0;
     cur.measure();
-    return true;
+    return cur.settle(p, per_row);
 }
 
 // Partial results: the slot of (block, item) is block + item's number, which
@@ -164,15 +181,18 @@ __host__ __device__ inline int64_t part_floats(int heads, int d) { return ((int6
 
 // ---- bf16 -----------------------------------------------------------------------
 
-// A warp's 32 rows of d bf16 in shared memory: boxes of at most 64 columns, in
-// each the rows one after the other, swizzled as TMA does it with the widest
-// pattern a row allows.  lane_offset is the place of (row r, 16-byte chunk hi)
-// of a 16-row half; k-step k (chunk 2k + hi) lies at that place with k's low
-// bits flipped in, because the swizzle is an exclusive or.
+constexpr int kBWarps = kRuns;               // warps that compute: one run of a tile each
+constexpr int kBThreads = kBWarps * 32;
+
+// A tile of d bf16 in shared memory: boxes of at most 64 columns, in each the
+// rows one after the other, swizzled as TMA does it with the widest pattern a
+// row allows.  lane_offset is the place of (row r, 16-byte chunk hi); k-step k
+// (chunk 2k + hi) lies at that place with k's low bits flipped in, because the
+// swizzle is an exclusive or.
 template <int D>
 struct TileLayout {
     static constexpr int RB = D >= 64 ? 128 : D * 2;   // bytes of a box row
-    static constexpr int BOX = kWarpPairs * RB;        // bytes of a box
+    static constexpr int BOX = kTile * RB;             // bytes of a box
     static constexpr int KPB = RB / 32;                // k-steps of a box
     __device__ __forceinline__ static uint32_t lane_offset(int r, int hi) {
         const int x = RB == 128 ? (r & 7) : RB == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
@@ -211,54 +231,53 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4}], [%2], "
+        "%5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "l"(policy)
         : "memory");
 }
 
 template <int D, int NT>
 struct Bf16Shape {
     static constexpr int STAGES = D >= 64 ? 3 : 4;
-    static constexpr int STAGE_BYTES = kWarpPairs * D * 2 * 2;  // one warp's keys and values
+    static constexpr int STAGE_BYTES = kTile * D * 2 * 2;  // a tile's keys and values
     static constexpr int HEADS = 8 * NT;
-    static constexpr int OS = D + 4;                    // floats between heads of a warp's outputs
-    static constexpr int RING = kWarps * STAGES * STAGE_BYTES;
-    static constexpr int SMEM = 1024 + RING + 2 * HEADS * OS * 4;
+    static constexpr int OS = D + 4;                       // floats between heads of a warp's outputs
+    static constexpr int SUMS = NT == 1 ? 4 : 2;           // buffers the warps' outputs are added in
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + SUMS * HEADS * OS * 4;
 };
 
-// What a stage holds for a warp: the pool rows of its two halves, and their
-// pairs (0: nothing was loaded).
-struct StageNote {
-    int row[2];
-    int pairs[2];
+// What a stage holds of a run: its pool row and its pairs (0: not loaded).
+struct RunNote {
+    int row, pairs;
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads + 32) attend_bf16_kernel(const __grid_constant__ CUtensorMap map_k,
-                                                                    const __grid_constant__ CUtensorMap map_v,
-                                                                    const __grid_constant__ AttendParams p, int box_rows) {
+__global__ void __launch_bounds__(kBThreads + 32) attend_bf16_kernel(const __grid_constant__ CUtensorMap map_k,
+                                                                     const __grid_constant__ CUtensorMap map_v,
+                                                                     const __grid_constant__ AttendParams p, int box_rows) {
     using S = Bf16Shape<D, NT>;
     using L = TileLayout<D>;
     constexpr int KS = D / 16;      // k-steps of a score, 16-wide blocks of the output
-    constexpr int HALF = kBox * L::RB;
     extern __shared__ unsigned char dyn[];
     __shared__ __align__(8) uint64_t s_full[S::STAGES], s_free[S::STAGES];
-    __shared__ StageNote s_note[S::STAGES][kWarps];
-    __shared__ float s_m[kWarps][S::HEADS], s_l[kWarps][S::HEADS];
+    __shared__ RunNote s_note[S::STAGES][kRuns];
+    __shared__ float s_m[kBWarps][S::HEADS], s_l[kBWarps][S::HEADS];
     __shared__ int s_abort;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int boxes = kTile / box_rows;  // of rows; one lane brings in each
     if (tid == 0) {
         for (int s = 0; s < S::STAGES; ++s) {
-            mbar_init(&s_full[s], kWarps);
-            mbar_init(&s_free[s], kWarps);
+            mbar_init(&s_full[s], boxes);
+            mbar_init(&s_free[s], kBWarps);
         }
         s_abort = 0;
         fence_mbar_init();
     }
-    if (tid == kThreads) {
+    if (tid == kBThreads) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
     }
@@ -266,23 +285,23 @@ __global__ void __launch_bounds__(kThreads + 32) attend_bf16_kernel(const __grid
     griddep_launch_dependents();
     const int per_row = p.c.H * p.items;
     Cursor cur;
-    if (!find_part<kWarps + 1>(p, per_row, cur)) return;  // its barriers also publish the mbarriers
+    if (!find_part<kBWarps + 1>(p, per_row, cur)) return;  // its barriers also publish the mbarriers
 
-    const uint32_t dyn0 = (smem_u32(dyn) + 1023u) & ~1023u;
-    if (warp == kWarps) {
-        // ---- loads: lane w brings in warp w's 32 pairs of every tile ---------------------
-        if (lane >= kWarps) return;
-        const int w = lane;
-        const bool whole = box_rows == kWarpPairs;  // one box holds both halves: a page does
-        int page0 = -1, page1 = -1;                 // table entries, fetched a tile early
-        int j = cur.tile * kTile + w * kWarpPairs, left = cur.count;
+    const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
+    if (warp == kBWarps) {
+        // ---- loads: a lane per box of rows ------------------------------------------------
+        if (lane >= boxes) return;
+        const int runs = box_rows / kRun, row0 = lane * box_rows;
+        int page = -1;  // table entry, fetched a tile early
+        int j = cur.tile * kTile + row0, left = cur.count;
         const int32_t *table = p.c.table + (int64_t)cur.b * p.c.max_pages;
         int head = (cur.item / p.items) * p.c.page;
-        auto fetch_pages = [&]() {
-            if (j < cur.n) page0 = table[p.c.page_of(j)];
-            if (j + kBox < cur.n) page1 = table[p.c.page_of(j + kBox)];
-        };
-        fetch_pages();
+        const int step = p.c.H * p.c.page;
+        if (j < cur.n) page = table[p.c.page_of(j)];
+        // keys and values are read once: they are the first to leave L2, so that
+        // the scores stay for the join
+        uint64_t policy;
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
         int st = 0;
         uint32_t round = 0;  // times the ring went around
         bool dead = false;
@@ -291,41 +310,35 @@ __global__ void __launch_bounds__(kThreads + 32) attend_bf16_kernel(const __grid
                 dead = true;
                 break;
             }
-            int n0 = max(0, min(kBox, cur.n - j)), n1 = max(0, min(kBox, cur.n - j - kBox));
-            if ((n0 && !page_ok(p.c, page0)) || (n1 && !page_ok(p.c, page1))) {
+            int n = max(0, min(box_rows, cur.n - j));
+            if (n && !page_ok(p.c, page)) {
                 report(p.c.status, TC_ERR_DEVICE_BOUNDS);
-                if (!page_ok(p.c, page0)) n0 = 0;
-                if (!page_ok(p.c, page1)) n1 = 0;
+                n = 0;
             }
-            const int step = p.c.H * p.c.page;
-            const int r0 = page0 * step + head + j - p.c.page_of(j) * p.c.page;
-            const int r1 = page1 * step + head + j + kBox - p.c.page_of(j + kBox) * p.c.page;
+            const int row = page * step + head + j - p.c.page_of(j) * p.c.page;
+            for (int i = 0; i < runs; ++i)
+                s_note[st][lane * runs + i] = RunNote{row + i * kRun, max(0, min(kRun, n - i * kRun))};
             uint64_t *bar = &s_full[st];
-            s_note[st][w] = StageNote{{r0, r1}, {n0, n1}};
-            const uint32_t dst = dyn0 + (w * S::STAGES + st) * S::STAGE_BYTES;
-            if (n0 | n1) mbar_expect_tx(bar, whole ? S::STAGE_BYTES : ((n0 ? 1 : 0) + (n1 ? 1 : 0)) * (S::STAGE_BYTES / 2));
-            else mbar_arrive(bar);
+            if (n) {
+                mbar_expect_tx(bar, (uint32_t)box_rows * D * 4);
+                const uint32_t dst = ring + st * S::STAGE_BYTES + row0 * L::RB;
 #pragma unroll
-            for (int x = 0; x * L::RB < D * 2; ++x) {
-                const uint32_t kd = dst + x * L::BOX, vd = kd + S::STAGE_BYTES / 2;
-                if (n0 || (whole && n1)) {
-                    tma_load_2d(kd, &map_k, bar, x * 64, r0);
-                    tma_load_2d(vd, &map_v, bar, x * 64, r0);
+                for (int x = 0; x * L::RB < D * 2; ++x) {
+                    tma_load_2d(dst + x * L::BOX, &map_k, bar, x * 64, row, policy);
+                    tma_load_2d(dst + S::STAGE_BYTES / 2 + x * L::BOX, &map_v, bar, x * 64, row, policy);
                 }
-                if (!whole && n1) {
-                    tma_load_2d(kd + HALF, &map_k, bar, x * 64, r1);
-                    tma_load_2d(vd + HALF, &map_v, bar, x * 64, r1);
-                }
+            } else {
+                mbar_arrive(bar);
             }
             j += kTile;
             if (--left == 0) {
-                more = cur.next(p, per_row);
-                j = cur.tile * kTile + w * kWarpPairs;
+                more = cur.next(p, per_row) && cur.settle(p, per_row);
+                j = cur.tile * kTile + row0;
                 left = cur.count;
                 table = p.c.table + (int64_t)cur.b * p.c.max_pages;
                 head = (cur.item / p.items) * p.c.page;
             }
-            if (more) fetch_pages();
+            if (more && j < cur.n) page = table[p.c.page_of(j)];
             if (++st == S::STAGES) {
                 st = 0;
                 ++round;
@@ -340,34 +353,35 @@ __global__ void __launch_bounds__(kThreads + 32) attend_bf16_kernel(const __grid
         return;
     }
 
-    const uint32_t ring = dyn0 + warp * S::STAGES * S::STAGE_BYTES;
-    float *s_o = reinterpret_cast<float *>(dyn + (dyn0 - smem_u32(dyn)) + S::RING);  // [2][HEADS][OS]
-    auto warps_sync = []() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
+    float *s_o = reinterpret_cast<float *>(dyn + (ring - smem_u32(dyn)) + S::STAGES * S::STAGE_BYTES);  // [SUMS][HEADS][OS]
+    auto warps_sync = []() { asm volatile("bar.sync 1, %0;" ::"n"(kBThreads) : "memory"); };
     const float scale = rsqrtf((float)D) * 1.4426950408889634f;  // log2(e)/sqrt(d)
-    const uint32_t k_lane = L::lane_offset((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
-    const uint32_t v_lane = L::lane_offset((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
+    const uint32_t k_lane = L::lane_offset(warp * kRun + (lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+    const uint32_t v_lane = L::lane_offset(warp * kRun + (lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1) + S::STAGE_BYTES / 2;
     const int c0 = (lane % 4) * 2, r0 = lane / 4;  // this lane's columns (heads) and first row (pair)
+    uint32_t qf[NT][KS][2];
+    auto load_q = [&]() {  // the queries of the cursor's stretch
+        const int h = cur.item / p.items, grp = cur.item - h * p.items;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int hh = grp * S::HEADS + t * 8 + r0;
+            const uint32_t *qp = reinterpret_cast<const uint32_t *>(p.q) + (((int64_t)cur.b * p.Hq + h * p.G + hh) * D + c0) / 2;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                qf[t][k][0] = hh < p.G ? qp[k * 8] : 0u;
+                qf[t][k][1] = hh < p.G ? qp[k * 8 + 4] : 0u;
+            }
+        }
+    };
+    load_q();
     uint32_t parity = 0;  // of the ring's round
     bool dead = false;
     int st = 0;
-    bool more = true;
-    while (more) {
+    for (bool more = true; more;) {
         // ---- one stretch: tiles of one (row, head, group of query heads) -----------
-        const int b = cur.b, h = cur.item / p.items, grp = cur.item - h * p.items;
-        const int h0 = h * p.G + grp * S::HEADS;  // first query head
+        const int grp = cur.item - cur.item / p.items * p.items;
         const int heads = min(S::HEADS, p.G - grp * S::HEADS);
-        const int64_t item = (int64_t)b * per_row + cur.item;
-        uint32_t qf[NT][KS][2];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int hh = t * 8 + r0;
-            const uint32_t *qp = reinterpret_cast<const uint32_t *>(p.q) + (((int64_t)b * p.Hq + h0 + hh) * D + c0) / 2;
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                qf[t][k][0] = hh < heads ? qp[k * 8] : 0u;
-                qf[t][k][1] = hh < heads ? qp[k * 8 + 4] : 0u;
-            }
-        }
+        const int64_t item = (int64_t)cur.b * per_row + cur.item;
         float m[NT][2], l[NT][2], o[NT][KS][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -381,10 +395,10 @@ __global__ void __launch_bounds__(kThreads + 32) attend_bf16_kernel(const __grid
         for (int i = 0; i < cur.count; ++i) {
             if (!dead && !mbar_wait(&s_full[st], parity, &s_abort, p.c.status, p.wait_ns)) dead = true;
             if (dead) break;
-            const StageNote note = s_note[st][warp];
-            if (note.pairs[0] | note.pairs[1]) {
-                const uint32_t ks = ring + st * S::STAGE_BYTES, vs = ks + S::STAGE_BYTES / 2;
-                // S^T = K Q^T of both halves
+            const RunNote note = s_note[st][warp];
+            if (note.pairs) {
+                const uint32_t base = ring + st * S::STAGE_BYTES;
+                // S^T = K Q^T, in two chains of products
                 float sc[NT][2][4];
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
@@ -392,48 +406,51 @@ __global__ void __launch_bounds__(kThreads + 32) attend_bf16_kernel(const __grid
                     for (int e = 0; e < 4; ++e) sc[t][0][e] = sc[t][1][e] = 0.f;
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
+                    uint32_t a[4];
+                    ldsm_x4(base + L::at(k_lane, k), a);
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        uint32_t a[4];
-                        ldsm_x4(ks + f * HALF + L::at(k_lane, k), a);
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) mma16816(sc[t][f], a, qf[t][k][0], qf[t][k][1]);
-                    }
+                    for (int t = 0; t < NT; ++t) mma16816(sc[t][k & 1], a, qf[t][k][0], qf[t][k][1]);
                 }
-                uint32_t ph[NT][2][2], pl[NT][2][2];
+                if (note.pairs < kRun) {
+                    // values of slots behind the row's pairs may hold anything, and
+                    // 0 * NaN is no 0: they are cleared
+                    constexpr int VPR = D / 8;  // 16-byte vectors of a row
+                    for (int x = lane; x < (kRun - note.pairs) * VPR; x += 32) {
+                        const int r = note.pairs + x / VPR, v = x % VPR;
+                        const uint32_t at = base + S::STAGE_BYTES / 2 + (v * 16 / L::RB) * L::BOX + (warp * kRun + r) * L::RB + v * 16 % L::RB;
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                uint32_t ph[NT][2], pl[NT][2];
                 bool grew = false;
                 float corr[NT][2];
-                const bool ragged = note.pairs[0] + note.pairs[1] < kWarpPairs;
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    float z[2][4];
+                    float z[4];
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) z[f][e] = sc[t][f][e] * scale;
-                        if (p.z) {
-                            // the group's scores of a pair lie side by side
-                            float *zr = p.z + ((int64_t)note.row[f] + r0) * p.G + grp * S::HEADS + t * 8 + c0;
-                            if (p.G % 2 == 0) {
-                                if (t * 8 + c0 < heads) {
-                                    if (r0 < note.pairs[f]) *reinterpret_cast<float2 *>(zr) = make_float2(z[f][0], z[f][1]);
-                                    if (r0 + 8 < note.pairs[f]) *reinterpret_cast<float2 *>(zr + 8 * p.G) = make_float2(z[f][2], z[f][3]);
-                                }
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (t * 8 + c0 + (e & 1) < heads && r0 + (e >> 1) * 8 < note.pairs[f])
-                                        zr[(e & 1) + (e >> 1) * 8 * p.G] = z[f][e];
+                    for (int e = 0; e < 4; ++e) z[e] = (sc[t][0][e] + sc[t][1][e]) * scale;
+                    if (p.z) {
+                        // the group's scores of a pair lie side by side
+                        float *zr = p.z + ((int64_t)note.row + r0) * p.G + grp * S::HEADS + t * 8 + c0;
+                        if (p.G % 2 == 0) {
+                            if (t * 8 + c0 < heads) {
+                                if (r0 < note.pairs) *reinterpret_cast<float2 *>(zr) = make_float2(z[0], z[1]);
+                                if (r0 + 8 < note.pairs) *reinterpret_cast<float2 *>(zr + 8 * p.G) = make_float2(z[2], z[3]);
                             }
-                        }
-                        if (ragged) {
-                            if (r0 >= note.pairs[f]) z[f][0] = z[f][1] = -INFINITY;
-                            if (r0 + 8 >= note.pairs[f]) z[f][2] = z[f][3] = -INFINITY;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (t * 8 + c0 + (e & 1) < heads && r0 + (e >> 1) * 8 < note.pairs)
+                                    zr[(e & 1) + (e >> 1) * 8 * p.G] = z[e];
                         }
                     }
+                    if (r0 >= note.pairs) z[0] = z[1] = -INFINITY;
+                    if (r0 + 8 >= note.pairs) z[2] = z[3] = -INFINITY;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = fmaxf(fmaxf(z[0][e], z[0][e + 2]), fmaxf(z[1][e], z[1][e + 2]));
+                        float x = fmaxf(z[e], z[e + 2]);
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -442,24 +459,19 @@ __global__ void __launch_bounds__(kThreads + 32) attend_bf16_kernel(const __grid
                         corr[t][e] = ex2(m[t][e] - ref);
                         grew |= mn > m[t][e];
                         m[t][e] = mn;
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            z[f][e] = ex2(z[f][e] - ref);
-                            z[f][e + 2] = ex2(z[f][e + 2] - ref);
-                        }
-                        l[t][e] = fmaf(l[t][e], corr[t][e], (z[0][e] + z[0][e + 2]) + (z[1][e] + z[1][e + 2]));
+                        z[e] = ex2(z[e] - ref);
+                        z[e + 2] = ex2(z[e + 2] - ref);
+                        l[t][e] = fmaf(l[t][e], corr[t][e], z[e] + z[e + 2]);
                     }
                     // P^T as a bf16 pair: hi rounded, lo the rest
 #pragma unroll
-                    for (int f = 0; f < 2; ++f)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float x = z[f][2 * e], y = z[f][2 * e + 1];
-                            const uint32_t hi = pack_bf16(x, y);
-                            const uint32_t lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
-                            ph[t][f][e] = transpose8x8(hi);
-                            pl[t][f][e] = transpose8x8(lo);
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = z[2 * e], y = z[2 * e + 1];
+                        const uint32_t hi = pack_bf16(x, y);
+                        const uint32_t lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+                        ph[t][e] = transpose8x8(hi);
+                        pl[t][e] = transpose8x8(lo);
+                    }
                 }
                 if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -470,26 +482,13 @@ __global__ void __launch_bounds__(kThreads + 32) attend_bf16_kernel(const __grid
                             for (int e = 0; e < 4; ++e) o[t][k][e] *= corr[t][e & 1];
                 }
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    // values of slots behind the row's pairs may hold anything: 0 * NaN
-                    const int nv = note.pairs[f];
-                    const uint32_t keep0 = (c0 < nv ? 0xffffu : 0u) | (c0 + 1 < nv ? 0xffff0000u : 0u);
-                    const uint32_t keep1 = (c0 + 8 < nv ? 0xffffu : 0u) | (c0 + 9 < nv ? 0xffff0000u : 0u);
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t a[4];
+                    ldsm_x4_t(base + L::at(v_lane, k), a);
 #pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        uint32_t a[4];
-                        ldsm_x4_t(vs + f * HALF + L::at(v_lane, k), a);
-                        if (ragged) {
-                            a[0] &= keep0;
-                            a[1] &= keep0;
-                            a[2] &= keep1;
-                            a[3] &= keep1;
-                        }
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            mma16816(o[t][k], a, ph[t][f][0], ph[t][f][1]);
-                            mma16816(o[t][k], a, pl[t][f][0], pl[t][f][1]);
-                        }
+                    for (int t = 0; t < NT; ++t) {
+                        mma16816(o[t][k], a, ph[t][0], ph[t][1]);
+                        mma16816(o[t][k], a, pl[t][0], pl[t][1]);
                     }
                 }
             }
@@ -500,6 +499,10 @@ __global__ void __launch_bounds__(kThreads + 32) attend_bf16_kernel(const __grid
                 parity ^= 1u;
             }
         }
+        // the next stretch's queries come in while this one's results are joined
+        const int block = (int)blockIdx.x;
+        more = cur.next(p, per_row) && cur.settle(p, per_row);
+        if (more) load_q();
         // ---- the warps' results, joined ----------------------------------------------
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -515,21 +518,25 @@ __global__ void __launch_bounds__(kThreads + 32) attend_bf16_kernel(const __grid
                 }
             }
         warps_sync();
-        // each warp scales its outputs to the common maximum; pairs of warps add
+        // each warp scales its outputs to the common maximum; SUMS warps at a time add
+        auto top = [&](int hh) {
+            float mx = s_m[0][hh];
+#pragma unroll
+            for (int w = 1; w < kBWarps; ++w) mx = fmaxf(mx, s_m[w][hh]);
+            return mx;
+        };
         float f[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int hh = t * 8 + c0 + e;
-                float mx = fmaxf(fmaxf(s_m[0][hh], s_m[1][hh]), fmaxf(s_m[2][hh], s_m[3][hh]));
-                if (mx == -INFINITY) mx = 0.f;
-                f[t][e] = ex2(m[t][e] - mx);
+                const float mx = top(t * 8 + c0 + e);
+                f[t][e] = ex2(m[t][e] - (mx == -INFINITY ? 0.f : mx));
             }
-        float *so = s_o + (warp & 1) * S::HEADS * S::OS;
+        float *so = s_o + (warp % S::SUMS) * S::HEADS * S::OS;
 #pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-            if ((warp >> 1) == pass) {
+        for (int pass = 0; pass < kBWarps / S::SUMS; ++pass) {
+            if (warp / S::SUMS == pass) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -543,31 +550,37 @@ __global__ void __launch_bounds__(kThreads + 32) attend_bf16_kernel(const __grid
             }
             warps_sync();
         }
-        float *part = p.part + (blockIdx.x + item) * part_floats(S::HEADS, D);
-        for (int x = tid; x < heads * D; x += kThreads) {
+        float *part = p.part + (block + item) * part_floats(S::HEADS, D);
+        for (int x = tid; x < heads * D; x += kBThreads) {
             const int hh = x / D, dd = x % D;
-            part[x] = s_o[hh * S::OS + dd] + s_o[(S::HEADS + hh) * S::OS + dd];
+            float sum = 0.f;
+#pragma unroll
+            for (int s = 0; s < S::SUMS; ++s) sum += s_o[(s * S::HEADS + hh) * S::OS + dd];
+            part[x] = sum;
         }
         if (tid < heads) {
-            const float mx = fmaxf(fmaxf(s_m[0][tid], s_m[1][tid]), fmaxf(s_m[2][tid], s_m[3][tid]));
+            const float mx = top(tid);
             float ls = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) ls += s_l[w][tid] * ex2(s_m[w][tid] - (mx == -INFINITY ? 0.f : mx));
+            for (int w = 0; w < kBWarps; ++w) ls += s_l[w][tid] * ex2(s_m[w][tid] - (mx == -INFINITY ? 0.f : mx));
             part[S::HEADS * D + 2 * tid] = mx;
             part[S::HEADS * D + 2 * tid + 1] = ls;
         }
         warps_sync();
-        more = cur.next(p, per_row);
     }
 }
 
 // ---- float32 ----------------------------------------------------------------------
 
+constexpr int kFWarps = 4;
+constexpr int kFThreads = kFWarps * 32;
+constexpr int kFPairs = kTile / kFWarps;  // pairs of a tile one warp takes
+
 template <int D, int GT>
-__global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(kFThreads) attend_f32_kernel(const __grid_constant__ AttendParams p) {
     constexpr int LPK = D / 4;                 // lanes per pair
     constexpr int KPW = 32 / LPK;              // pairs a warp loads at once
-    constexpr int NG = kWarps * KPW;           // groups of lanes with statistics of their own
+    constexpr int NG = kFWarps * KPW;           // groups of lanes with statistics of their own
     constexpr int BATCH = 4;                   // loads of keys in flight per lane (and of values)
     __shared__ float s_m[NG][GT], s_l[NG][GT];
     __shared__ __align__(16) float s_o[NG][GT][D];
@@ -577,7 +590,7 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
     griddep_launch_dependents();
     const int per_row = p.c.H * p.items;
     Cursor cur;
-    if (!find_part<kWarps>(p, per_row, cur)) return;
+    if (!find_part<kFWarps>(p, per_row, cur)) return;
     const float scale = rsqrtf((float)D) * 1.4426950408889634f;
     const float *kpool = reinterpret_cast<const float *>(p.c.k), *vpool = reinterpret_cast<const float *>(p.c.v);
     bool more = true;
@@ -597,8 +610,8 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
         }
         // the warp's 32 pairs of each tile, as two runs of 16 within a page
         for (int i2 = 0; i2 < 2 * cur.count; ++i2) {
-            const int j0 = (cur.tile + i2 / 2) * kTile + warp * kWarpPairs + (i2 & 1) * kBox;
-            int nv = max(0, min(kBox, cur.n - j0));
+            const int j0 = (cur.tile + i2 / 2) * kTile + warp * kFPairs + (i2 & 1) * kRun;
+            int nv = max(0, min(kRun, cur.n - j0));
             int64_t row = 0;
             if (nv) {
                 const int pi = p.c.page_of(j0), pg = p.c.table[(int64_t)b * p.c.max_pages + pi];
@@ -610,14 +623,14 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
                 }
             }
 #pragma unroll
-            for (int u = 0; u < kBox / KPW; u += BATCH) {
+            for (int u = 0; u < kRun / KPW; u += BATCH) {
                 if (u * KPW >= nv) break;
                 float4 k4[BATCH], v4[BATCH];
 #pragma unroll
                 for (int i = 0; i < BATCH; ++i) {
                     const int j = (u + i) * KPW + sub;
                     k4[i] = v4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (u + i < kBox / KPW && j < nv) {
+                    if (u + i < kRun / KPW && j < nv) {
                         k4[i] = reinterpret_cast<const float4 *>(kpool)[(row + j) * LPK + li];
                         v4[i] = reinterpret_cast<const float4 *>(vpool)[(row + j) * LPK + li];
                     }
@@ -634,7 +647,7 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
 #pragma unroll
                         for (int off = LPK / 2; off >= 1; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
                         const int j = (u + i) * KPW + sub;
-                        const bool in = u + i < kBox / KPW && j < nv;
+                        const bool in = u + i < kRun / KPW && j < nv;
                         z[i] = x * scale;
                         if (p.z && in && li == 0 && g < heads) p.z[(row + j) * p.G + grp * GT + g] = z[i];
                         if (!in) z[i] = -INFINITY;
@@ -669,7 +682,7 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
         }
         __syncthreads();
         float *part = p.part + (blockIdx.x + item) * part_floats(GT, D);
-        for (int x = tid; x < heads * D; x += kThreads) {
+        for (int x = tid; x < heads * D; x += kFThreads) {
             const int g = x / D, dd = x % D;
             float mx = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -689,7 +702,7 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
             part[GT * D + 2 * tid + 1] = sum;
         }
         __syncthreads();
-        more = cur.next(p, per_row);
+        more = cur.next(p, per_row) && cur.settle(p, per_row);
     }
 }
 
@@ -712,10 +725,11 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
     constexpr int CHUNK = 64;                 // partials whose factors are held at a time
     constexpr int OUT = (HB * D + kJoinThreads - 1) / kJoinThreads;  // outputs per thread
     __shared__ __align__(16) float s_red[RG][HB][D];
-    constexpr int WU = 4;                     // pairs per thread in flight (weights)
-    __shared__ float s_q[HB][D], s_f[HB][CHUNK], s_m[kMassStats], s_l[kMassStats];
+    constexpr int WU = kTile / 32;            // pairs per lane in flight (weights)
+    __shared__ float s_q[HB][D], s_f[HB][CHUNK];
+    __shared__ __align__(16) float s_m[kMassStats], s_l[kMassStats];
     __shared__ int s_b[kMassTiles], s_h[kMassTiles], s_t[kMassTiles];
-    __shared__ int s_row[kMassTiles * (kTile / kBox)], s_nv[kMassTiles * (kTile / kBox)];
+    __shared__ int s_row[kMassTiles * (kTile / kRun)], s_nv[kMassTiles * (kTile / kRun)];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const CacheParams &c = p.c;
     const int per_row = c.H * p.items;
@@ -814,7 +828,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
                 if (tiles > 0) {
                     const Cut cut((uint32_t)p.prefix[c.B] * per_row, js.split_grid);
                     const int grp = g0 / p.heads, hh = g0 % p.heads;  // a batch never crosses a group
-                    const uint32_t u0 = (uint32_t)p.prefix[b] * per_row + (h * p.items + grp) * tiles;
+                    const uint32_t u0 = (uint32_t)p.prefix[b] * per_row + (h * p.items + grp) * (tiles + kExtra);
                     const int p0 = (int)cut.block_of(u0), np = (int)cut.block_of(u0 + tiles - 1) - p0 + 1;
                     const float *part = p.part + (p0 + (int64_t)b * per_row + h * p.items + grp) * pf;
                     __syncthreads();
@@ -880,8 +894,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
 
     // ---- weights: this block's share of the tiles of every (row, key/value head) -----
     // A chunk of tiles at a time: which (row, head) each belongs to, the
-    // joined maximum and sum of every query head of each, then the pairs, WU per
-    // thread in flight.
+    // joined maximum and sum of every query head of each, then the pairs.
     griddep_wait();
     int *s_pre = reinterpret_cast<int *>(&s_red[0][0][0]);  // rows' prefix, where it fits
     const uint32_t all = (uint32_t)p.prefix[c.B];
@@ -906,16 +919,16 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
                 if (pre[mid] * c.H <= x) lo = mid;
                 else hi = mid - 1;
             }
-            const int tiles = pre[lo + 1] - pre[lo], off = x - pre[lo] * c.H;
+            const int units = pre[lo + 1] - pre[lo], off = x - pre[lo] * c.H;
             s_b[tid] = lo;
-            s_h[tid] = off / tiles;
-            s_t[tid] = off - s_h[tid] * tiles;
+            s_h[tid] = off / units;
+            s_t[tid] = off - s_h[tid] * units;  // the last kExtra hold no pairs
         }
         __syncthreads();
         // pool row and pairs of every run of 16
-        for (int x = tid; x < nt * (kTile / kBox); x += kJoinThreads) {
-            const int i = x / (kTile / kBox), b = s_b[i], j = s_t[i] * kTile + x % (kTile / kBox) * kBox;
-            int nv = max(0, min(kBox, (int)row_pairs(p, b) - j)), row = 0;
+        for (int x = tid; x < nt * (kTile / kRun); x += kJoinThreads) {
+            const int i = x / (kTile / kRun), b = s_b[i], j = s_t[i] * kTile + x % (kTile / kRun) * kRun;
+            int nv = max(0, min(kRun, (int)row_pairs(p, b) - j)), row = 0;
             if (nv) {
                 const int pi = c.page_of(j), pg = c.table[(int64_t)b * c.max_pages + pi];
                 if (page_ok(c, pg)) row = (pg * c.H + s_h[i]) * c.page + j - pi * c.page;
@@ -931,8 +944,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
             const bool lead = x < nt * p.G && (i == 0 || s_t[i] == 0);
             float M = -INFINITY, L = 0.f;
             if (lead) {
-                const int tiles = pre[b + 1] - pre[b], grp = g / p.heads, hh = g - grp * p.heads;
-                const uint32_t u0 = (uint32_t)pre[b] * per_row + (h * p.items + grp) * tiles;
+                const int units = pre[b + 1] - pre[b], tiles = units - kExtra, grp = g / p.heads, hh = g - grp * p.heads;
+                const uint32_t u0 = (uint32_t)pre[b] * per_row + (h * p.items + grp) * units;
                 const int p0 = (int)cut.block_of(u0), np = (int)cut.block_of(u0 + tiles - 1) - p0 + 1;
                 const float *ml = p.part + (p0 + (int64_t)b * per_row + h * p.items + grp) * pf + p.heads * D + 2 * hh;
 #pragma unroll 4
@@ -956,20 +969,15 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
             }
         }
         __syncthreads();
-        for (int j0 = tid; j0 < nt * kTile; j0 += WU * kJoinThreads) {
-            int row[WU], stat[WU];
-#pragma unroll
-            for (int k = 0; k < WU; ++k) {
-                const int x = j0 + k * kJoinThreads, i = x / kTile, q = x / kBox;
-                row[k] = -1;
-                if (i < nt) {
-                    stat[k] = (i - min(i, s_t[i])) * p.G;  // the (row, head)'s first tile of the chunk
-                    if (x % kBox < s_nv[q]) row[k] = s_row[q] + x % kBox;
-                }
-            }
+        // a warp per tile, WU pairs a lane: the statistics are the warp's
+        for (int i = warp; i < nt; i += kJoinThreads / 32) {
+            const int stat = (i - min(i, s_t[i])) * p.G;  // of the (row, head)'s first tile of the chunk
+            int row[WU];
             float w[WU], old[WU];
 #pragma unroll
             for (int k = 0; k < WU; ++k) {
+                const int x = k * 32 + lane, q = i * kRuns + x / kRun;
+                row[k] = x % kRun < s_nv[q] ? s_row[q] + x % kRun : -1;
                 w[k] = 0.f;
                 if (row[k] >= 0) old[k] = c.mass[row[k]];
             }
@@ -979,15 +987,14 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
 #pragma unroll
                     for (int k = 0; k < WU; ++k)
                         if (row[k] >= 0) z[k] = *reinterpret_cast<const float4 *>(p.z + (int64_t)row[k] * p.G + g);
+                    const float4 m4 = *reinterpret_cast<const float4 *>(&s_m[stat + g]), l4 = *reinterpret_cast<const float4 *>(&s_l[stat + g]);
 #pragma unroll
-                    for (int k = 0; k < WU; ++k)
-                        if (row[k] >= 0) {
-                            const int s = stat[k] + g;
-                            w[k] = fmaf(ex2(z[k].x - s_m[s]), s_l[s], w[k]);
-                            w[k] = fmaf(ex2(z[k].y - s_m[s + 1]), s_l[s + 1], w[k]);
-                            w[k] = fmaf(ex2(z[k].z - s_m[s + 2]), s_l[s + 2], w[k]);
-                            w[k] = fmaf(ex2(z[k].w - s_m[s + 3]), s_l[s + 3], w[k]);
-                        }
+                    for (int k = 0; k < WU; ++k) {
+                        w[k] = fmaf(ex2(z[k].x - m4.x), l4.x, w[k]);
+                        w[k] = fmaf(ex2(z[k].y - m4.y), l4.y, w[k]);
+                        w[k] = fmaf(ex2(z[k].z - m4.z), l4.z, w[k]);
+                        w[k] = fmaf(ex2(z[k].w - m4.w), l4.w, w[k]);
+                    }
                 }
             } else {
                 for (int g = 0; g < p.G; ++g) {
@@ -995,9 +1002,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
 #pragma unroll
                     for (int k = 0; k < WU; ++k)
                         if (row[k] >= 0) z[k] = p.z[(int64_t)row[k] * p.G + g];
+                    const float m1 = s_m[stat + g], l1 = s_l[stat + g];
 #pragma unroll
-                    for (int k = 0; k < WU; ++k)
-                        if (row[k] >= 0) w[k] = fmaf(ex2(z[k] - s_m[stat[k] + g]), s_l[stat[k] + g], w[k]);
+                    for (int k = 0; k < WU; ++k) w[k] = fmaf(ex2(z[k] - m1), l1, w[k]);
                 }
             }
 #pragma unroll
@@ -1058,23 +1065,23 @@ template <int D, int NT>
 cudaError_t split_bf16(const AttendParams &p, int num_sms, int *grid, cudaStream_t s) {
     CUtensorMap mk, mv;
     const int64_t rows = (int64_t)p.c.n_pages * p.c.H * p.c.page;
-    // a warp's 32 pairs are in one page, or in two halves that may be in two
-    const int box_rows = p.c.page % kWarpPairs == 0 ? kWarpPairs : kBox;
+    int box_rows = kRun;  // rows that always share a page: the fewer loads, the larger they are
+    while (box_rows < kTile && p.c.page % (2 * box_rows) == 0) box_rows *= 2;
     if (!make_pool_map(&mk, p.c.k, rows, D, box_rows) || !make_pool_map(&mv, p.c.v, rows, D, box_rows))
         return cudaErrorInvalidValue;
-    cudaError_t e = fill_grid(attend_bf16_kernel<D, NT>, kThreads + 32, Bf16Shape<D, NT>::SMEM, num_sms, grid);
+    cudaError_t e = fill_grid(attend_bf16_kernel<D, NT>, kBThreads + 32, Bf16Shape<D, NT>::SMEM, num_sms, grid);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = early_launch(&attr, *grid, kThreads + 32, Bf16Shape<D, NT>::SMEM, s, p.step);
+    const cudaLaunchConfig_t cfg = early_launch(&attr, *grid, kBThreads + 32, Bf16Shape<D, NT>::SMEM, s, p.step);
     return cudaLaunchKernelEx(&cfg, attend_bf16_kernel<D, NT>, mk, mv, p, box_rows);
 }
 
 template <int D, int GT>
 cudaError_t split_f32(const AttendParams &p, int num_sms, int *grid, cudaStream_t s) {
-    cudaError_t e = fill_grid(attend_f32_kernel<D, GT>, kThreads, 0, num_sms, grid);
+    cudaError_t e = fill_grid(attend_f32_kernel<D, GT>, kFThreads, 0, num_sms, grid);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = early_launch(&attr, *grid, kThreads, 0, s, p.step);
+    const cudaLaunchConfig_t cfg = early_launch(&attr, *grid, kFThreads, 0, s, p.step);
     return cudaLaunchKernelEx(&cfg, attend_f32_kernel<D, GT>, p);
 }
 
@@ -1126,7 +1133,7 @@ size_t attend_part_bytes(int64_t BH, int G, int d, tc_dtype dtype, int num_sms) 
     return (size_t)(attend_grid(num_sms) + items) * (size_t)part_floats(heads, d) * sizeof(float);
 }
 
-double attend_units(double items, int64_t capacity) { return items * (double)((capacity + kTile - 1) / kTile); }
+double attend_units(double items, int64_t capacity) { return items * (double)((capacity + kTile - 1) / kTile + kExtra); }
 
 bool attend_supported(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
