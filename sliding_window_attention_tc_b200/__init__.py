@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -172,9 +173,10 @@ _lib.tc_prefill_path_for.argtypes = [_PD, ctypes.c_int64]
 _lib.tc_prefill_path_for.restype = _int
 
 _PC, _PR = ctypes.POINTER(PagedCacheC), ctypes.POINTER(RotaryC)
-_lib.tc_rotate.argtypes = [ctypes.POINTER(RotateDesc), _PR, _vp, ctypes.c_int64] + [_vp] * 4 + [_vp]
+# the small per-call structures go as packed bytes (or by reference): see _PACK_*
+_lib.tc_rotate.argtypes = [_vp, _PR, _vp, ctypes.c_int64] + [_vp] * 4 + [_vp]
 _lib.tc_rotate.restype = _int
-_lib.tc_cache_append.argtypes = [_PC, _PR, ctypes.POINTER(AppendArgs), _vp]
+_lib.tc_cache_append.argtypes = [_PC, _PR, _vp, _vp]
 _lib.tc_cache_append.restype = _int
 _lib.tc_cache_attend_workspace_size.argtypes = [_PC, ctypes.c_int64, ctypes.c_uint32]
 _lib.tc_cache_attend_workspace_size.restype = _sz
@@ -186,7 +188,7 @@ _lib.tc_cache_evict.argtypes = [_PC, ctypes.c_int64, ctypes.c_int64, _vp, _sz, _
 _lib.tc_cache_evict.restype = _int
 _lib.tc_cache_step_workspace_size.argtypes = [_PC, ctypes.c_int64, ctypes.c_uint32]
 _lib.tc_cache_step_workspace_size.restype = _sz
-_lib.tc_cache_step.argtypes = [_PC, _PR, ctypes.POINTER(StepArgs), _vp, _sz, _vp]
+_lib.tc_cache_step.argtypes = [_PC, _PR, _vp, _vp, _sz, _vp]
 _lib.tc_cache_step.restype = _int
 
 SIZE_ERROR = ctypes.c_size_t(-1).value
@@ -736,55 +738,74 @@ class Rotary:
         raise AttributeError("Rotary is immutable")
 
 
-def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+# tc_rotate_desc, tc_append_args and tc_step_args as struct formats: packing them
+# takes a tenth of the time that filling a ctypes structure does, and a call of a
+# few microseconds feels it.
+_PACK_ROTATE = struct.Struct("=5qiI12q")
+_PACK_APPEND = struct.Struct("=2q3Q9q3Q")
+_PACK_STEP = struct.Struct("=q3Q6q2Q2qI4x")
+assert (_PACK_ROTATE.size, _PACK_APPEND.size, _PACK_STEP.size) == tuple(
+    ctypes.sizeof(s) for s in (RotateDesc, AppendArgs, StepArgs))
 
 
-def _rows(t: Optional[torch.Tensor], name: str, shape, dtype):
-    """[b,h,t,d] rows with a contiguous head dimension; returns the strides."""
+def _addr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _raw_stream(dev: int, *ts, stream=None):
+    """The stream to launch on, for tensors that must all be on CUDA device
+    `dev`, the current one."""
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}; the call's other tensors are on "
+                             f"{'the CPU' if dev < 0 else f'cuda:{dev}'}")
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    if torch._C._cuda_getDevice() != dev:
+        raise ValueError(f"tensors on cuda:{dev} but the current CUDA device is cuda:{torch.cuda.current_device()}; "
+                         "call under torch.cuda.device(...) of the tensors' device")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype):
+    """Rows [..., d] with a contiguous head dimension; returns the strides."""
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}; expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
     s = t.stride()
-    if s[3] != 1 and shape[3] > 1:
+    if s[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the head dimension must be contiguous")
-    return s[:3]
-
-
-def _token_rows(t: torch.Tensor, name: str, shape, dtype):
-    """[b,h,d] rows with a contiguous head dimension; returns the strides."""
-    _expect(t, name, shape, dtype)
-    s = t.stride()
-    if s[2] != 1 and shape[2] > 1:
-        raise ValueError(f"{name}: the head dimension must be contiguous")
-    return s[:2]
+    return s[:-1]
 
 
 def _rotate(q, k, rotary, positions, t0, q_out, k_out, flags, stream):
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q and k must be [B,heads,T,d]")
-    B, Hq, T, d = q.shape
-    dt = _dtype_code(q)
-    H = 0 if k is None else k.shape[1]
+    qn, dtype = q.shape, q.dtype
+    B, Hq, T, d = qn
+    H = 0
     if q_out is None:
-        q_out = torch.empty((B, Hq, T, d), dtype=q.dtype, device=q.device)
-    qs, qos = _rows(q, "q", q.shape, q.dtype), _rows(q_out, "q_out", q.shape, q.dtype)
+        q_out = torch.empty(qn, dtype=dtype, device=q.device)
+    qs, qos = _rows(q, "q", qn, dtype), _rows(q_out, "q_out", qn, dtype)
     ks = kos = (0, 0, 0)
     if k is not None:
+        H = k.shape[1]
+        kn = (B, H, T, d)
         if k_out is None:
-            k_out = torch.empty((B, H, T, d), dtype=q.dtype, device=q.device)
-        ks, kos = _rows(k, "k", (B, H, T, d), q.dtype), _rows(k_out, "k_out", (B, H, T, d), q.dtype)
+            k_out = torch.empty(kn, dtype=dtype, device=q.device)
+        ks, kos = _rows(k, "k", kn, dtype), _rows(k_out, "k_out", kn, dtype)
     elif k_out is not None:
         raise ValueError("k_out without k")
     if positions is not None:
         _expect(positions, "positions", (B, T), torch.int64)
         _contig(positions)
-    _dev_check(q, k, q_out, k_out, positions)
-    desc = RotateDesc(B, Hq, H, T, d, dt, flags, _I3(*qs), _I3(*ks), _I3(*qos), _I3(*kos))
-    _check(_lib.tc_rotate(ctypes.byref(desc), rotary.ref, None if positions is None else positions.data_ptr(),
-                          int(t0), q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-                          None if k is None else k_out.data_ptr(), _raw_stream(stream)), "tc_rotate")
+    desc = _PACK_ROTATE.pack(B, Hq, H, T, d, _dtype_code(q), flags, *qs, *ks, *qos, *kos)
+    s = _raw_stream(q.get_device(), k, q_out, k_out, positions, stream=stream)
+    st = _lib.tc_rotate(desc, rotary.ref, _addr(positions), int(t0), q.data_ptr(), _addr(k), q_out.data_ptr(),
+                        _addr(k_out), s)
+    if st:
+        raise TCError(st, "tc_rotate")
     return q_out, k_out
 
 
@@ -820,7 +841,7 @@ class PagedCache:
     cannot be exchanged afterwards (their contents can)."""
 
     __slots__ = ("k_pages", "v_pages", "table", "lens", "clocks", "mass", "pos", "A", "lam", "eta",
-                 "c", "ref", "B", "H", "d", "dtype", "device")
+                 "c", "ref", "B", "H", "d", "dtype", "device", "dev")
 
     def __init__(self, k_pages, v_pages, table, lens, clocks, *, mass=None, pos=None, A=None, lam=None,
                  eta=None):
@@ -850,7 +871,8 @@ class PagedCache:
         p = [None if t is None else t.data_ptr() for t in ts]
         c = PagedCacheC(B, H, d, page, n_pages, max_pages, dt, p[0], p[1], p[5], p[6], p[2], p[3], p[4],
                         p[7], p[8] if A is not None else None, p[9] if A is not None else None)
-        for name, x in zip(self.__slots__, ts + (c, ctypes.pointer(c), B, H, d, k_pages.dtype, k_pages.device)):
+        for name, x in zip(self.__slots__, ts + (c, ctypes.pointer(c), B, H, d, k_pages.dtype, k_pages.device,
+                                               k_pages.get_device())):
             object.__setattr__(self, name, x)
 
     def __setattr__(self, name, value):
@@ -872,17 +894,6 @@ class PagedCache:
                           pos=torch.zeros((n_pages, H, page), dtype=torch.int32, device=device),
                           A=None if lam is None else torch.zeros((B, H, d, d), **f), lam=lam, eta=eta)
 
-    def here(self, *ts):
-        """The other tensors of a call are where the cache is, and that is the
-        current device."""
-        dev = self.device
-        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-            raise ValueError(f"the cache is on {dev} but the current CUDA device is "
-                             f"cuda:{torch.cuda.current_device()}")
-        for t in ts:
-            if t is not None and t.device != dev:
-                raise ValueError(f"tensor on {t.device}; the cache is on {dev}")
-
 
 def _workspace(size: int, where: str, workspace, device):
     if size == SIZE_ERROR:
@@ -891,7 +902,7 @@ def _workspace(size: int, where: str, workspace, device):
         workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=device)
     elif not workspace.is_contiguous():
         raise ValueError("tensors must be contiguous")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.nbytes
 
 
 def _new_workspace(size: int, where: str, cache):
@@ -910,7 +921,8 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, rotary:
     if k.dim() != 4:
         raise ValueError("k must be [B,H,T,d]")
     B, H, d, T = cache.B, cache.H, cache.d, k.shape[2]
-    ks, vs = _rows(k, "k", (B, H, T, d), cache.dtype), _rows(v, "v", (B, H, T, d), cache.dtype)
+    kn = (B, H, T, d)
+    ks, vs = _rows(k, "k", kn, cache.dtype), _rows(v, "v", kn, cache.dtype)
     qs, Hq = (0, 0, 0), 0
     if q is not None:
         if q.dim() != 4:
@@ -925,11 +937,12 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, rotary:
     _expect(counts, "counts", (B,), torch.int64)
     _expect(mass, "mass", (B, H, T), torch.float32)
     _contig(counts, mass, q_out)
-    cache.here(k, v, q, q_out, counts, mass)
-    p = [None if t is None else t.data_ptr() for t in (q, counts, mass, q_out)]
-    a = AppendArgs(T, Hq, p[0], k.data_ptr(), v.data_ptr(), _I3(*qs), _I3(*ks), _I3(*vs), p[1], p[2], p[3])
-    _check(_lib.tc_cache_append(cache.ref, None if rotary is None else rotary.ref, ctypes.byref(a),
-                                _raw_stream(stream)), "tc_cache_append")
+    s = _raw_stream(cache.dev, k, v, q, q_out, counts, mass, stream=stream)
+    a = _PACK_APPEND.pack(T, Hq, _addr(q), k.data_ptr(), v.data_ptr(), *qs, *ks, *vs, _addr(counts), _addr(mass),
+                          _addr(q_out))
+    st = _lib.tc_cache_append(cache.ref, None if rotary is None else rotary.ref, a, s)
+    if st:
+        raise TCError(st, "tc_cache_append")
     return q_out
 
 
@@ -959,9 +972,10 @@ def cache_attend(cache: PagedCache, q: torch.Tensor, *, g: Optional[torch.Tensor
     n = 0 if workspace is not None else _lib.tc_cache_attend_workspace_size(cache.ref, Hq, flags)
     workspace, room = _workspace(n, "tc_cache_attend_workspace_size", workspace, cache.device)
     _contig(q, g, y)
-    cache.here(q, g, y, workspace)
-    _check(_lib.tc_cache_attend(cache.ref, Hq, q.data_ptr(), None if g is None else g.data_ptr(), y.data_ptr(),
-                                flags, workspace.data_ptr(), room, _raw_stream(stream)), "tc_cache_attend")
+    s = _raw_stream(cache.dev, q, g, y, workspace, stream=stream)
+    st = _lib.tc_cache_attend(cache.ref, Hq, q.data_ptr(), _addr(g), y.data_ptr(), flags, workspace.data_ptr(), room, s)
+    if st:
+        raise TCError(st, "tc_cache_attend")
     return y
 
 
@@ -969,7 +983,7 @@ def _query_heads(cache: PagedCache, q: torch.Tensor) -> int:
     if q.dim() != 3:
         raise ValueError("q must be [B,Hq,d]")
     Hq = q.shape[1]
-    _expect(q, "q", (cache.B, Hq, cache.d), cache.dtype)
+    _rows(q, "q", (cache.B, Hq, cache.d), cache.dtype)
     if Hq < 1 or Hq % cache.H:
         raise ValueError(f"{Hq} query heads over {cache.H} key/value heads")
     return Hq
@@ -989,9 +1003,8 @@ def cache_evict(cache: PagedCache, budget: int, *, recent: int = 1,
         raise ValueError("eviction needs a cache with mass and pos")
     n = 0 if workspace is not None else _lib.tc_cache_evict_workspace_size(cache.ref)
     workspace, room = _workspace(n, "tc_cache_evict_workspace_size", workspace, cache.device)
-    cache.here(workspace)
-    _check(_lib.tc_cache_evict(cache.ref, int(budget), int(recent), workspace.data_ptr(), room,
-                               _raw_stream(stream)), "tc_cache_evict")
+    s = _raw_stream(cache.dev, workspace, stream=stream)
+    _check(_lib.tc_cache_evict(cache.ref, int(budget), int(recent), workspace.data_ptr(), room, s), "tc_cache_evict")
 
 
 def cache_step_workspace(cache: PagedCache, Hq: int, *, accumulate: bool = True) -> torch.Tensor:
@@ -1010,8 +1023,8 @@ def cache_step(cache: PagedCache, q: torch.Tensor, k: torch.Tensor, v: torch.Ten
     q, k and v may have any strides with a contiguous head dimension.  Returns
     y [B,Hq,d]."""
     Hq = _query_heads(cache, q)
-    qs, ks, vs = (_token_rows(t, n, (cache.B, h, cache.d), cache.dtype)
-                  for t, n, h in ((q, "q", Hq), (k, "k", cache.H), (v, "v", cache.H)))
+    kn = (cache.B, cache.H, cache.d)
+    qs, ks, vs = _rows(q, "q", (cache.B, Hq, cache.d), cache.dtype), _rows(k, "k", kn, cache.dtype), _rows(v, "v", kn, cache.dtype)
     _expect(g, "g", (Hq,), torch.float32)
     if g is not None and cache.A is None:
         raise ValueError("g reads the memory, but the cache has none")
@@ -1024,11 +1037,12 @@ def cache_step(cache: PagedCache, q: torch.Tensor, k: torch.Tensor, v: torch.Ten
     n = 0 if workspace is not None else _lib.tc_cache_step_workspace_size(cache.ref, Hq, flags)
     workspace, room = _workspace(n, "tc_cache_step_workspace_size", workspace, cache.device)
     _contig(g, y)
-    cache.here(q, k, v, g, y, workspace)
-    a = StepArgs(Hq, q.data_ptr(), k.data_ptr(), v.data_ptr(), _I2(*qs), _I2(*ks), _I2(*vs),
-                 None if g is None else g.data_ptr(), y.data_ptr(), int(budget), int(recent), flags)
-    _check(_lib.tc_cache_step(cache.ref, None if rotary is None else rotary.ref, ctypes.byref(a),
-                              workspace.data_ptr(), room, _raw_stream(stream)), "tc_cache_step")
+    s = _raw_stream(cache.dev, q, k, v, g, y, workspace, stream=stream)
+    a = _PACK_STEP.pack(Hq, q.data_ptr(), k.data_ptr(), v.data_ptr(), *qs, *ks, *vs, _addr(g), y.data_ptr(), int(budget),
+                        int(recent), flags)
+    st = _lib.tc_cache_step(cache.ref, None if rotary is None else rotary.ref, a, workspace.data_ptr(), room, s)
+    if st:
+        raise TCError(st, "tc_cache_step")
     return y
 
 

@@ -30,7 +30,7 @@
 
 #include <cuda.h>
 
-#include <cfloat>
+#include <atomic>
 
 #include "paged_cache.cuh"
 #include "sm100_ptx.cuh"
@@ -1035,18 +1035,31 @@ bool make_pool_map(CUtensorMap *m, const void *base, int64_t rows, int d, int bo
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Resident blocks of a kernel over the device, at most attend_grid's bound.
-template <typename K>
-cudaError_t fill_grid(K kernel, int threads, int smem, int num_sms, int *grid) {
-    cudaError_t e = smem > 0 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
-    if (e != cudaSuccess) return e;
-    int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
-    if (e != cudaSuccess) return e;
-    const int most = attend_grid(num_sms);
-    *grid = per_sm * num_sms < most ? per_sm * num_sms : most;
-    return *grid > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
-}
+// Resident blocks of a kernel over the current device, at most attend_grid's
+// bound.  Asked of the driver (and the shared memory granted) once per kernel
+// and device: it takes longer than the launch.
+struct ResidentGrid {
+    static constexpr int kDevices = 64;
+    std::atomic<int> per_sm[kDevices];
+    template <typename K>
+    cudaError_t get(K kernel, int threads, int smem, int num_sms, int *grid) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        int n = dev < kDevices ? per_sm[dev].load(std::memory_order_acquire) : 0;
+        if (n == 0) {
+            e = allow_smem(kernel, (size_t)smem);
+            if (e != cudaSuccess) return e;
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, (size_t)smem);
+            if (e != cudaSuccess) return e;
+            if (n < 1) return cudaErrorInvalidConfiguration;
+            if (dev < kDevices) per_sm[dev].store(n, std::memory_order_release);
+        }
+        const int most = attend_grid(num_sms);
+        *grid = n * num_sms < most ? n * num_sms : most;
+        return cudaSuccess;
+    }
+};
 
 cudaLaunchConfig_t early_launch(cudaLaunchAttribute *attr, int grid, int threads, int smem, cudaStream_t s, bool early) {
     attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1069,7 +1082,8 @@ cudaError_t split_bf16(const AttendParams &p, int num_sms, int *grid, cudaStream
     while (box_rows < kTile && p.c.page % (2 * box_rows) == 0) box_rows *= 2;
     if (!make_pool_map(&mk, p.c.k, rows, D, box_rows) || !make_pool_map(&mv, p.c.v, rows, D, box_rows))
         return cudaErrorInvalidValue;
-    cudaError_t e = fill_grid(attend_bf16_kernel<D, NT>, kBThreads + 32, Bf16Shape<D, NT>::SMEM, num_sms, grid);
+    static ResidentGrid resident;
+    cudaError_t e = resident.get(attend_bf16_kernel<D, NT>, kBThreads + 32, Bf16Shape<D, NT>::SMEM, num_sms, grid);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = early_launch(&attr, *grid, kBThreads + 32, Bf16Shape<D, NT>::SMEM, s, p.step);
@@ -1078,7 +1092,8 @@ cudaError_t split_bf16(const AttendParams &p, int num_sms, int *grid, cudaStream
 
 template <int D, int GT>
 cudaError_t split_f32(const AttendParams &p, int num_sms, int *grid, cudaStream_t s) {
-    cudaError_t e = fill_grid(attend_f32_kernel<D, GT>, kFThreads, 0, num_sms, grid);
+    static ResidentGrid resident;
+    cudaError_t e = resident.get(attend_f32_kernel<D, GT>, kFThreads, 0, num_sms, grid);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = early_launch(&attr, *grid, kFThreads, 0, s, p.step);
