@@ -400,16 +400,21 @@ __global__ void __launch_bounds__(kOneThreads) evict_one_kernel(const __grid_con
 
 // ---- several pairs leave ------------------------------------------------------------
 //
-// The pairs are sorted by leave_key (bitonic, in shared memory up to kSortMax),
-// and the weighted sum runs on the tensor cores: tiles of TP pairs come in by
-// asynchronous 16-byte copies, double buffered; the weighted keys
+// The slots are sorted by (protected, mass, pos) with a stable radix sort of 8
+// bits a pass, in shared memory up to kSortMax pairs; passes whose digit is the
+// same for every pair (most of the positions' and the protection's) are skipped.
+// (A bitonic sort of 4096 keys with their slots took 139,000 cycles.)  The
+// weighted sum runs on the tensor cores: tiles of TP pairs come in by
+// asynchronous 16-byte copies, several in flight; the weighted keys
 // lambda^(m-1-i) k_i are split into three bf16 parts (24 bits together; a
 // float32 cache's values too), and the products' sums over one tile are added
 // to float32 sums with the ordinary rounding, because the tensor cores' own
-// accumulation truncates and would drift over thousands of pairs.
+// accumulation truncates and would drift over thousands of pairs.  The blocks
+// of a cluster take every SL-th tile and add their sums through one another's
+// shared memory.
 constexpr int kBulkThreads = 512;
 constexpr int kBulkWarps = kBulkThreads / 32;
-constexpr int kSortMax = 8192;   // pairs sorted in shared memory (12 bytes each)
+constexpr int kSortMax = 8192;   // pairs sorted in shared memory (16 bytes each)
 
 // lambda^j for j >= 0 to float32's precision: the exponent in 64 bits, its
 // fraction to exp2f.
@@ -427,28 +432,6 @@ struct Decay {
         return negative && (j & 1) ? -r : r;
     }
 };
-
-// Bitonic sort of n2 (a power of two) keys with their slots, ascending.
-__device__ void block_sort(uint64_t *key, uint32_t *slot, int n2) {
-    for (int size = 2; size <= n2; size *= 2) {
-        for (int stride = size / 2; stride > 0; stride /= 2) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < n2 / 2; i += kBulkThreads) {
-                const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
-                const bool up = (lo & size) == 0;
-                const uint64_t ka = key[lo], kb = key[hi];
-                const uint32_t sa = slot[lo], sb = slot[hi];
-                if (less_pair(kb, sb, ka, sa) == up) {
-                    key[lo] = kb;
-                    key[hi] = ka;
-                    slot[lo] = sb;
-                    slot[hi] = sa;
-                }
-            }
-        }
-    }
-    __syncthreads();
-}
 
 // Exclusive prefix of one count per thread over the block; *total the sum.
 __device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
@@ -470,6 +453,57 @@ __device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
     }
     *total = all;
     return before + v - x;
+}
+
+// One stable pass of 8 bits: order b of n slots from order a by (key[slot] >>
+// shift) & 255.  Each warp counts the digits of its share, the counts' prefix
+// over (digit, warp) gives every element its place.  False (and b untouched)
+// when all digits are the same.
+__device__ bool radix_pass(const uint32_t *key, const uint32_t *a, uint32_t *b, int n, int shift, uint32_t *counts, int *scan) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int share = (n + kBulkWarps * 32 - 1) / (kBulkWarps * 32) * 32, i0 = warp * share, i1 = min(n, i0 + share);
+    uint32_t *mine = counts + warp * 256;
+    __syncthreads();
+    for (int x = tid; x < kBulkWarps * 256; x += kBulkThreads) counts[x] = 0;
+    __syncthreads();
+    for (int i = i0 + lane; i < i0 + share; i += 32) {
+        const uint32_t d = i < i1 ? (key[a[i]] >> shift) & 255u : 256u;
+        const uint32_t same = __match_any_sync(0xffffffffu, d);
+        if (d < 256u && (same & ((1u << lane) - 1u)) == 0) mine[d] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    int sum = 0, total;
+    if (tid < 256) {
+#pragma unroll
+        for (int w = 0; w < kBulkWarps; ++w) sum += counts[w * 256 + tid];
+    }
+    if (__syncthreads_or(sum == n)) return false;
+    int at = block_scan(sum, scan, &total);
+    if (tid < 256) {
+#pragma unroll
+        for (int w = 0; w < kBulkWarps; ++w) {
+            const int c = (int)counts[w * 256 + tid];
+            counts[w * 256 + tid] = (uint32_t)at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    for (int i = i0 + lane; i < i0 + share; i += 32) {
+        const uint32_t s = i < i1 ? a[i] : 0u;
+        const uint32_t d = i < i1 ? (key[s] >> shift) & 255u : 256u;
+        const uint32_t same = __match_any_sync(0xffffffffu, d);
+        const uint32_t before = __popc(same & ((1u << lane) - 1u));
+        const uint32_t base = d < 256u ? mine[d] : 0u;
+        __syncwarp();
+        if (d < 256u) {
+            b[base + before] = s;
+            if (before == 0) mine[d] = base + __popc(same);
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    return true;
 }
 
 __device__ __forceinline__ void ldsm_t4(const void *p, uint32_t (&r)[4]) {
@@ -506,30 +540,39 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t (&o)[3]) {
     }
 }
 
-// Shared memory of one block: raw tiles (two), the parts, sorting room.
-template <typename T, int D, int SL>
+// Shared memory of one block: the order of the pairs, then, one after the
+// other in the same room, what sorting needs (keys, positions, a second order,
+// counts), what the sum needs (raw tiles, parts; its result), and the lists of
+// moves.
+template <typename T, int D>
 struct BulkShape {
-    static constexpr int R = D / SL;                        // rows of A
     static constexpr int TP = sizeof(T) == 2 ? 64 : 32;     // pairs per tile
+    static constexpr int STAGES = 3;
     static constexpr int VPARTS = sizeof(T) == 2 ? 0 : 3;   // bf16 values go in as they are
-    static constexpr int KRAW = R * (int)sizeof(T);         // bytes of a raw row
+    static constexpr int KRAW = D * (int)sizeof(T);         // bytes of a raw row
     static constexpr int VRAW = D * (int)sizeof(T) + 16;    // padded: conflict-free reads by ldmatrix
-    static constexpr int KS = R * 2 + 16, VS = D * 2 + 16;  // bytes of a row of a part
+    static constexpr int PS = D * 2 + 16;                   // bytes of a row of a part
     static constexpr int RAW = TP * (KRAW + VRAW);
-    static constexpr int PARTS = TP * (3 * KS + VPARTS * VS);
-    static constexpr int SMEM = 2 * RAW + PARTS;            // the sorting room follows
+    static constexpr int PARTS = TP * (3 + VPARTS) * PS;
+    static constexpr int SUM = STAGES * RAW + PARTS;        // at least the result's 4 D^2
     // output tiles of 16 x 8: warps along the rows first
-    static constexpr int TM = R / 16, TN = D / 8, NWN = kBulkWarps / TM;
+    static constexpr int TM = D / 16, TN = D / 8, NWN = kBulkWarps / TM;
     static constexpr int NT = TN / NWN > 0 ? TN / NWN : 1;  // tiles a warp holds
+    static_assert(SUM >= 4 * D * D, "the block's sum has to fit");
 };
 
+// Bytes of sorting room for up to n pairs (a multiple of 32): keys, positions,
+// second order; with the counts, and the first order, which stays.
+__host__ __device__ constexpr size_t sort_room(size_t n) { return 12 * n + kBulkWarps * 256 * 4; }
+__host__ __device__ constexpr size_t order_room(size_t n) { return (4 * n + n / 8 + 127) / 128 * 128; }  // and a bit per slot
+
 template <typename T, int D, int SL>
-__global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_constant__ EvictParams p, int n2_cap) {
-    using S = BulkShape<T, D, SL>;
+__global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_constant__ EvictParams p, int n_cap) {
+    using S = BulkShape<T, D>;
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ int s_scan[kBulkWarps];
-    __shared__ int64_t s_row[2][S::TP];
-    __shared__ float s_w[2][S::TP];
+    __shared__ int s_row[S::STAGES + 1][S::TP];
+    __shared__ float s_w[S::STAGES + 1][S::TP];
 
     const CacheParams &c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -545,38 +588,81 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_c
     const int32_t *table = c.table + (int64_t)b * c.max_pages;
     auto row_of = [&](int slot) {
         const int pg = c.page_of(slot);
-        return pool_row(c, table[pg], h, slot - pg * c.page);
+        return (int)pool_row(c, table[pg], h, slot - pg * c.page);
     };
     T *kp = reinterpret_cast<T *>(c.k), *vp = reinterpret_cast<T *>(c.v);
 
     // ---- the order of leaving -----------------------------------------------------
-    const int64_t protect_from = c.clock[b] - p.recent;
-    int n2 = 1;
-    while (n2 < n) n2 *= 2;
-    const bool inside = n2 <= n2_cap;
-    const int room = inside ? n2_cap : n2_cap_global(c.capacity());
-    unsigned char *ws = inside ? dyn + S::SMEM : p.sort_ws + (bh * SL + rank) * (size_t)room * 13;
-    uint64_t *key = reinterpret_cast<uint64_t *>(ws);
-    uint32_t *slot = reinterpret_cast<uint32_t *>(ws + (size_t)room * 8);
-    uint32_t *bits = reinterpret_cast<uint32_t *>(ws + (size_t)room * 12);
+    const bool inside = n <= n_cap;
+    const size_t room = inside ? n_cap : n2_cap_global(c.capacity());
+    unsigned char *kept = inside ? dyn : p.sort_ws + (bh * SL + rank) * (order_room(room) + sort_room(room));
+    unsigned char *scratch = kept + order_room(room);     // sorting and lists
+    unsigned char *tiles_mem = dyn + order_room(n_cap);   // the sum
+    uint32_t *order = reinterpret_cast<uint32_t *>(kept), *bits = order + room;
+    uint32_t *weight = reinterpret_cast<uint32_t *>(scratch), *place = weight + room, *other = place + room;
+    uint32_t *counts = other + room;
     const int words = (n + 31) / 32;
-    for (int s = tid; s < n2; s += kBulkThreads) {
-        uint64_t x = ~0ull;
-        if (s < n) {
-            const int64_t row = row_of(s);
-            x = leave_key(c.mass[row], c.pos[row], protect_from);
+    {
+        const int64_t protect_from = c.clock[b] - p.recent;
+        bool sorted = true;  // by position already, as tokens are appended
+        uint32_t prot_any = 0, prot_all = 1;
+        constexpr int U = 4;
+        for (int s0 = tid; s0 < n; s0 += U * kBulkThreads) {
+            float w[U];
+            int32_t z[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int s = s0 + i * kBulkThreads;
+                if (s < n) {
+                    const int row = row_of(s);
+                    w[i] = c.mass[row];
+                    z[i] = c.pos[row];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int s = s0 + i * kBulkThreads;
+                if (s < n) {
+                    const uint64_t key = leave_key(w[i], z[i], protect_from);
+                    weight[s] = (uint32_t)(key >> 31);
+                    // the position, and above it the protection
+                    place[s] = (uint32_t)(key & 0x7fffffffu) | (uint32_t)(key >> 63) << 31;
+                    order[s] = s;
+                    prot_any |= (uint32_t)(key >> 63);
+                    prot_all &= (uint32_t)(key >> 63);
+                }
+            }
         }
-        key[s] = x;
-        slot[s] = s < n ? (uint32_t)s : 0xffffffffu;
+        for (int s = tid; s < words; s += kBulkThreads) bits[s] = 0;
+        __syncthreads();
+        for (int s = tid; s + 1 < n; s += kBulkThreads)
+            sorted = sorted && (place[s] & 0x7fffffffu) <= (place[s + 1] & 0x7fffffffu);
+        const bool by_place = !__syncthreads_and(sorted);
+        const bool split = __syncthreads_or(prot_any) && !__syncthreads_and(prot_all);
+        uint32_t *from = order, *to = other;
+        auto pass = [&](const uint32_t *key, int shift) {
+            if (radix_pass(key, from, to, n, shift, counts, s_scan)) {
+                uint32_t *x = from;
+                from = to;
+                to = x;
+            }
+        };
+        // least significant first.  (The protection rides in the positions' top
+        // digit, which changes nothing: it is the last criterion again.)
+        if (by_place)
+            for (int shift = 0; shift < 32; shift += 8) pass(place, shift);
+        for (int shift = 0; shift < 32; shift += 8) pass(weight, shift);
+        if (split) pass(place, 31);
+        __syncthreads();
+        if (from != order)
+            for (int i = tid; i < n; i += kBulkThreads) order[i] = from[i];
+        __syncthreads();
     }
-    for (int s = tid; s < words; s += kBulkThreads) bits[s] = 0;
-    block_sort(key, slot, n2);
 
-    // ---- A's slice: lambda^m A + eta sum of lambda^(m-1-i) k_i v_i^T ----------------
+    // ---- A: lambda^m A + eta sum of lambda^(m-1-i) k_i v_i^T -------------------------
     if (c.A) {
         const Decay decay(c.lam[h]);
-        const int row0 = rank * S::R;
-        unsigned char *parts = dyn + 2 * S::RAW;
+        unsigned char *parts = tiles_mem + S::STAGES * S::RAW;
         const int wm = warp % S::TM, wn = (warp / S::TM) * S::NT;
         const bool works = wn < S::TN;
         float sum[S::NT][4];
@@ -584,67 +670,58 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_c
         for (int t = 0; t < S::NT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[t][e] = 0.f;
-        const int tiles = (m + S::TP - 1) / S::TP;
+        const int all = (m + S::TP - 1) / S::TP, tiles = (all - rank + SL - 1) / SL;  // every SL-th is this block's
         // pool rows and weights of a tile's pairs
         auto plan = [&](int tile) {
-            if (tid < S::TP) {
-                const int i = tile * S::TP + tid;
-                s_row[tile & 1][tid] = i < m ? row_of((int)slot[i]) : -1;
-                s_w[tile & 1][tid] = i < m ? decay.pow(m - 1 - i) : 0.f;
+            if (tid < S::TP && tile < tiles) {
+                const int i = (tile * SL + rank) * S::TP + tid;
+                s_row[tile % (S::STAGES + 1)][tid] = i < m ? row_of((int)order[i]) : -1;
+                s_w[tile % (S::STAGES + 1)][tid] = i < m ? decay.pow(m - 1 - i) : 0.f;
             }
         };
         auto fetch = [&](int tile) {
-            unsigned char *raw = dyn + (tile & 1) * S::RAW;
-            constexpr int KC = S::KRAW / 16, VC = D * (int)sizeof(T) / 16;
-            for (int x = tid; x < S::TP * (KC + VC); x += kBulkThreads) {
-                const int pr = x / (KC + VC), ch = x % (KC + VC);
-                const int64_t row = s_row[tile & 1][pr];
-                unsigned char *dst = ch < KC ? raw + pr * S::KRAW + ch * 16 : raw + S::TP * S::KRAW + pr * S::VRAW + (ch - KC) * 16;
-                const T *src = ch < KC ? kp + row * D + row0 + ch * (16 / (int)sizeof(T)) : vp + row * D + (ch - KC) * (16 / (int)sizeof(T));
-                if (row >= 0) copy16(dst, src);
-                else zero16(dst);
+            if (tile < tiles) {
+                unsigned char *raw = tiles_mem + (tile % S::STAGES) * S::RAW;
+                constexpr int RC = D * (int)sizeof(T) / 16, EL = 16 / (int)sizeof(T);  // chunks of a row, elements of one
+                for (int x = tid; x < S::TP * 2 * RC; x += kBulkThreads) {
+                    const int pr = x / (2 * RC), ch = x % (2 * RC);
+                    const int64_t row = s_row[tile % (S::STAGES + 1)][pr];
+                    unsigned char *dst = ch < RC ? raw + pr * S::KRAW + ch * 16 : raw + S::TP * S::KRAW + pr * S::VRAW + (ch - RC) * 16;
+                    const T *src = ch < RC ? kp + row * D + ch * EL : vp + row * D + (ch - RC) * EL;
+                    if (row >= 0) copy16(dst, src);
+                    else zero16(dst);
+                }
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            asm volatile("cp.async.commit_group;" ::: "memory");  // an empty group past the last tile
         };
-        plan(0);
+        for (int i = 0; i < S::STAGES; ++i) plan(i);
         __syncthreads();
-        fetch(0);
-        if (tiles > 1) plan(1);
+        for (int i = 0; i < S::STAGES - 1; ++i) fetch(i);
         for (int tile = 0; tile < tiles; ++tile) {
-            __syncthreads();  // the next tile's plan is there, the other buffer and the parts are free
-            if (tile + 1 < tiles) {
-                fetch(tile + 1);
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-            } else {
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
-            }
-            __syncthreads();
-            const unsigned char *raw = dyn + (tile & 1) * S::RAW;
-            for (int x = tid; x < S::TP * S::R / 2; x += kBulkThreads) {
-                const int pr = x / (S::R / 2), e = x % (S::R / 2);
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 2) : "memory");
+            __syncthreads();  // the tile is there; the parts and the last tile's buffer are free
+            fetch(tile + S::STAGES - 1);
+            plan(tile + S::STAGES);
+            const unsigned char *raw = tiles_mem + (tile % S::STAGES) * S::RAW;
+            for (int x = tid; x < S::TP * D / 2; x += kBulkThreads) {
+                const int pr = x / (D / 2), e = x % (D / 2);
                 const T *src = reinterpret_cast<const T *>(raw + pr * S::KRAW) + 2 * e;
-                const float w = s_w[tile & 1][pr];
+                const float w = s_w[tile % (S::STAGES + 1)][pr];
                 uint32_t o[3];
                 split3(w * to_f32(src[0]), w * to_f32(src[1]), o);
 #pragma unroll
-                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(parts + i * S::TP * S::KS + pr * S::KS + e * 4) = o[i];
-            }
-            if (S::VPARTS) {
-                for (int x = tid; x < S::TP * D / 2; x += kBulkThreads) {
-                    const int pr = x / (D / 2), e = x % (D / 2);
-                    const T *src = reinterpret_cast<const T *>(raw + S::TP * S::KRAW + pr * S::VRAW) + 2 * e;
-                    uint32_t o[3];
-                    split3(to_f32(src[0]), to_f32(src[1]), o);
+                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(parts + (i * S::TP + pr) * S::PS + e * 4) = o[i];
+                if (S::VPARTS) {
+                    const T *val = reinterpret_cast<const T *>(raw + S::TP * S::KRAW + pr * S::VRAW) + 2 * e;
+                    split3(to_f32(val[0]), to_f32(val[1]), o);
 #pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        *reinterpret_cast<uint32_t *>(parts + 3 * S::TP * S::KS + i * S::TP * S::VS + pr * S::VS + e * 4) = o[i];
+                    for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(parts + ((3 + i) * S::TP + pr) * S::PS + e * 4) = o[i];
                 }
             }
             __syncthreads();
-            if (tile + 2 < tiles) plan(tile + 2);
             if (works) {
-                const unsigned char *vbase = S::VPARTS ? parts + 3 * S::TP * S::KS : raw + S::TP * S::KRAW;
-                constexpr int VROW = S::VPARTS ? S::VS : S::VRAW;
+                const unsigned char *vbase = S::VPARTS ? parts + 3 * S::TP * S::PS : raw + S::TP * S::KRAW;
+                constexpr int VROW = S::VPARTS ? S::PS : S::VRAW;
                 float acc[S::NT][4];
 #pragma unroll
                 for (int t = 0; t < S::NT; ++t)
@@ -656,13 +733,13 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_c
                     uint32_t a[3][4];
 #pragma unroll
                     for (int i = 0; i < 3; ++i)
-                        ldsm_t4(parts + i * S::TP * S::KS + (k * 16 + (lane & 7) + (lane >> 4) * 8) * S::KS + (wm * 16 + ((lane >> 3) & 1) * 8) * 2, a[i]);
+                        ldsm_t4(parts + (i * S::TP + k * 16 + (lane & 7) + (lane >> 4) * 8) * S::PS + (wm * 16 + ((lane >> 3) & 1) * 8) * 2, a[i]);
 #pragma unroll
                     for (int t = 0; t < S::NT; ++t) {
 #pragma unroll
                         for (int j = 0; j < (S::VPARTS ? 3 : 1); ++j) {
                             uint32_t v[2];
-                            ldsm_t2(vbase + j * S::TP * S::VS + (k * 16 + (lane & 15)) * VROW + (wn + t) * 16, v);
+                            ldsm_t2(vbase + (j * S::TP + k * 16 + (lane & 15)) * VROW + (wn + t) * 16, v);
 #pragma unroll
                             for (int i = 2 - j; i >= 0; --i) mma_bf16(acc[t], a[i], v);
                         }
@@ -674,25 +751,65 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_c
                     for (int e = 0; e < 4; ++e) sum[t][e] += acc[t][e];
             }
         }
-        if (works) {
-            const float lm = decay.pow(m), eta = c.eta[h];
+        const float lm = decay.pow(m), eta = c.eta[h];
+        const int row = wm * 16 + lane / 4, col = (lane % 4) * 2;
+        if constexpr (SL == 1) {
+            if (works) {
 #pragma unroll
-            for (int t = 0; t < S::NT; ++t)
+                for (int t = 0; t < S::NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    float2 *x = reinterpret_cast<float2 *>(c.A + (bh * D + row0 + wm * 16 + lane / 4 + e * 4) * D + (wn + t) * 8 + (lane % 4) * 2);
-                    float2 o = *x;
-                    o.x = fmaf(lm, o.x, eta * sum[t][e]);
-                    o.y = fmaf(lm, o.y, eta * sum[t][e + 1]);
-                    *x = o;
+                    for (int e = 0; e < 4; e += 2) {
+                        float2 *x = reinterpret_cast<float2 *>(c.A + (bh * D + row + e * 4) * D + (wn + t) * 8 + col);
+                        float2 o = *x;
+                        o.x = fmaf(lm, o.x, eta * sum[t][e]);
+                        o.y = fmaf(lm, o.y, eta * sum[t][e + 1]);
+                        *x = o;
+                    }
+            }
+        } else {
+            float *mine = reinterpret_cast<float *>(tiles_mem);  // [D][D]
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();
+            if (works) {
+#pragma unroll
+                for (int t = 0; t < S::NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2)
+                        *reinterpret_cast<float2 *>(mine + (row + e * 4) * D + (wn + t) * 8 + col) = make_float2(sum[t][e], sum[t][e + 1]);
+            }
+            cluster_sync();
+            // this block's rows of A, from every block's sum
+            constexpr int R = D / SL;
+            for (int x = tid; x < R * D / 4; x += kBulkThreads) {
+                const int at = rank * R * D / 4 + x;
+                float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int r = 0; r < SL; ++r) {
+                    uint32_t there;
+                    float4 y;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(sm100::smem_u32(mine + at * 4)), "r"(r));
+                    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w) : "r"(there) : "memory");
+                    add.x += y.x;
+                    add.y += y.y;
+                    add.z += y.z;
+                    add.w += y.w;
                 }
+                float4 *dst = reinterpret_cast<float4 *>(c.A + bh * D * D) + at;
+                float4 o = *dst;
+                o.x = fmaf(lm, o.x, eta * add.x);
+                o.y = fmaf(lm, o.y, eta * add.y);
+                o.z = fmaf(lm, o.z, eta * add.z);
+                o.w = fmaf(lm, o.w, eta * add.w);
+                *dst = o;
+            }
+            cluster_sync();  // the sums have been read: their room is free
         }
     }
 
     // ---- freed slots below keep, and the pairs behind it that stay ------------------
-    for (int i = tid; i < m; i += kBulkThreads) atomicOr(&bits[slot[i] / 32], 1u << (slot[i] % 32));
-    __syncthreads();  // the keys are done with: their room takes the two lists
-    int *hole = reinterpret_cast<int *>(key), *fill = hole + room;
+    for (int i = tid; i < m; i += kBulkThreads) atomicOr(&bits[order[i] / 32], 1u << (order[i] % 32));
+    __syncthreads();
+    int *hole = reinterpret_cast<int *>(scratch), *fill = hole + room;
     const int per = (words + kBulkThreads - 1) / kBulkThreads;
     auto freed = [&](int w) {  // slots of word w that leave and are below keep
         const int below = keep - w * 32;
@@ -714,8 +831,13 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_c
     int ih = block_scan(nh, s_scan, &moves);
     int jf = block_scan(nf, s_scan, &total);
     for (int w = tid * per; w < min(words, (tid + 1) * per); ++w) {
-        for (uint32_t x = freed(w); x; x &= x - 1) hole[ih++] = (int)row_of(w * 32 + __ffs(x) - 1);
-        for (uint32_t x = stays(w); x; x &= x - 1) fill[jf++] = (int)row_of(w * 32 + __ffs(x) - 1);
+        for (uint32_t x = freed(w); x; x &= x - 1) hole[ih++] = w * 32 + __ffs(x) - 1;
+        for (uint32_t x = stays(w); x; x &= x - 1) fill[jf++] = w * 32 + __ffs(x) - 1;
+    }
+    __syncthreads();
+    for (int x = tid; x < 2 * moves; x += kBulkThreads) {  // slots to pool rows
+        int *at = x < moves ? hole + x : fill + (x - moves);
+        *at = row_of(*at);
     }
 
     // ---- moves, once every block of the cluster has read what they overwrite --------
@@ -782,7 +904,8 @@ template <typename T, int D, int SL>
 cudaError_t launch_bulk(const EvictParams &p, cudaStream_t s) {
     const int64_t cap = n2_cap_global(p.c.capacity());
     const int n2 = (int)(cap < kSortMax ? cap : kSortMax);
-    const size_t smem = BulkShape<T, D, SL>::SMEM + (size_t)n2 * 13;
+    const size_t sum = BulkShape<T, D>::SUM, sort = sort_room(n2);
+    const size_t smem = order_room(n2) + (sum > sort ? sum : sort);
     cudaError_t e = allow_smem(evict_bulk_kernel<T, D, SL>, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
@@ -852,7 +975,7 @@ int bulk_slices(int64_t BH, int d, int num_sms) { return slices_for(BH, d, 1, 4,
 
 size_t evict_sort_bytes(int64_t BH, int d, int64_t capacity, int num_sms) {
     const int64_t n2 = n2_cap_global(capacity);
-    return n2 <= kSortMax ? 0 : (size_t)BH * (size_t)bulk_slices(BH, d, num_sms) * (size_t)n2 * 13;
+    return n2 <= kSortMax ? 0 : (size_t)BH * (size_t)bulk_slices(BH, d, num_sms) * (order_room(n2) + sort_room(n2));
 }
 
 cudaError_t launch_cache_step_insert(const EvictParams &p, tc_dtype dtype, int d, int slices, cudaStream_t s) {

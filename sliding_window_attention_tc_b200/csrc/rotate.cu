@@ -83,18 +83,21 @@ bool make_rotary_table(const tc_rotary *r, int64_t d, RotaryTable *out) {
     out->rot = (int)r->rot;
     out->interleaved = (int)r->interleaved;
     out->gain = (float)r->gain;
-    const long double two_pi = 6.283185307179586476925286766559L;
+    const long double to_turns = 1.0L / 6.283185307179586476925286766559L;
+    const long double slow = 1.0L / (long double)r->factor;
+    const bool ramp = r->high > r->low;
+    const long double width = ramp ? 1.0L / ((long double)r->high - r->low) : 0.0L;
     // f_i by repeated products (63 at most, each off by 2^-64): a powl per
     // pair would cost more than the launch
     const long double ratio = out->rot ? powl((long double)r->base, -2.0L / (long double)r->rot) : 0.0L;
     long double f = 1.0L;
     for (int i = 0; i < out->rot / 2; ++i, f *= ratio) {
         long double keep = 0.0L;
-        if (r->high > r->low) {
-            keep = ((long double)r->train_len * f / two_pi - r->low) / ((long double)r->high - r->low);
+        if (ramp) {
+            keep = ((long double)r->train_len * f * to_turns - r->low) * width;
             keep = keep < 0.0L ? 0.0L : keep > 1.0L ? 1.0L : keep;
         }
-        const long double turns = f * (keep + (1.0L - keep) / r->factor) / two_pi;  // at most 1/(2 pi)
+        const long double turns = f * (keep + (1.0L - keep) * slow) * to_turns;  // at most 1/(2 pi)
         out->inc[i] = (uint64_t)(turns * 18446744073709551616.0L + 0.5L);
     }
     return true;
