@@ -17,6 +17,8 @@
 // cores) and stores the new lengths, which the first has to leave for its other
 // blocks to read.
 
+#include <type_traits>
+
 #include "paged_cache.cuh"
 #include "sm100_ptx.cuh"
 
@@ -26,6 +28,7 @@ namespace {
 // ---- insertion ------------------------------------------------------------------
 
 constexpr int kAppThreads = 256;
+constexpr int kAppUnroll = 4;
 
 // Tokens row b appends, or -1 when the row is to be skipped (and not because
 // it is empty: *bad says that an error has to be reported).  Block-wide.
@@ -62,38 +65,45 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
         RotChunk<VEC> rc;
         rc.place(p.table, chunk, d);
         rc.angles(p.table, chunk, position, false);
-        // rows: the queries' heads, the keys', the values' (copied)
-        const int rows = (p.q ? p.Hq : 0) + 2 * H, q_rows = p.q ? p.Hq : 0;
-        for (int x = hg; x < rows; x += HG) {
-            const T *src;
-            T *dst;
-            bool turn = true;
-            if (x < q_rows) {
-                src = reinterpret_cast<const T *>(p.q) + b * p.qs[0] + x * p.qs[1] + t * p.qs[2];
-                dst = reinterpret_cast<T *>(p.q_out) + (((int64_t)b * p.Hq + x) * p.T + t) * d;
-            } else {
-                const bool value = x - q_rows >= H;
-                const int h = x - q_rows - (value ? H : 0);
-                const int64_t row = pool_row(p.c, pg, h, in_page);
-                if (value) {
-                    src = reinterpret_cast<const T *>(p.v) + b * p.vs[0] + h * p.vs[1] + t * p.vs[2];
-                    dst = reinterpret_cast<T *>(p.c.v) + row * d;
-                    turn = false;
-                } else {
-                    src = reinterpret_cast<const T *>(p.k) + b * p.ks[0] + h * p.ks[1] + t * p.ks[2];
-                    dst = reinterpret_cast<T *>(p.c.k) + row * d;
-                    if (chunk == 0) {
-                        if (p.c.mass) p.c.mass[row] = p.mass_in ? p.mass_in[((int64_t)b * H + h) * p.T + t] : 0.f;
-                        if (p.c.pos) p.c.pos[row] = (int32_t)position;
-                    }
+        // rows: the queries' heads, the keys', the values' (copied); kAppUnroll in flight
+        const int q_rows = p.q ? p.Hq : 0, rows = q_rows + 2 * H;
+        for (int x0 = hg; x0 < rows; x0 += kAppUnroll * HG) {
+            float u[kAppUnroll][VEC], w[kAppUnroll][VEC];
+#pragma unroll
+            for (int i = 0; i < kAppUnroll; ++i) {
+                const int x = x0 + i * HG;
+                if (x < rows) {
+                    const T *src = x < q_rows       ? reinterpret_cast<const T *>(p.q) + b * p.qs[0] + x * p.qs[1] + t * p.qs[2]
+                                   : x < q_rows + H ? reinterpret_cast<const T *>(p.k) + b * p.ks[0] + (x - q_rows) * p.ks[1] + t * p.ks[2]
+                                                    : reinterpret_cast<const T *>(p.v) + b * p.vs[0] + (x - q_rows - H) * p.vs[1] + t * p.vs[2];
+                    Row<T, VEC>::load(src + rc.a, u[i]);
+                    if (rc.b >= 0) Row<T, VEC>::load(src + rc.b, w[i]);
                 }
             }
-            float u[VEC], w[VEC];
-            Row<T, VEC>::load(src + rc.a, u);
-            if (rc.b >= 0) Row<T, VEC>::load(src + rc.b, w);
-            if (turn) rc.turn(u, w);
-            Row<T, VEC>::store(dst + rc.a, u);
-            if (rc.b >= 0) Row<T, VEC>::store(dst + rc.b, w);
+#pragma unroll
+            for (int i = 0; i < kAppUnroll; ++i) {
+                const int x = x0 + i * HG;
+                if (x < rows) {
+                    T *dst;
+                    if (x < q_rows) {
+                        dst = reinterpret_cast<T *>(p.q_out) + (((int64_t)b * p.Hq + x) * p.T + t) * d;
+                        rc.turn(u[i], w[i]);
+                    } else if (x < q_rows + H) {
+                        const int h = x - q_rows;
+                        const int64_t row = pool_row(p.c, pg, h, in_page);
+                        dst = reinterpret_cast<T *>(p.c.k) + row * d;
+                        rc.turn(u[i], w[i]);
+                        if (chunk == 0) {
+                            if (p.c.mass) p.c.mass[row] = p.mass_in ? p.mass_in[((int64_t)b * H + h) * p.T + t] : 0.f;
+                            if (p.c.pos) p.c.pos[row] = (int32_t)position;
+                        }
+                    } else {
+                        dst = reinterpret_cast<T *>(p.c.v) + pool_row(p.c, pg, x - q_rows - H, in_page) * d;
+                    }
+                    Row<T, VEC>::store(dst + rc.a, u[i]);
+                    if (rc.b >= 0) Row<T, VEC>::store(dst + rc.b, w[i]);
+                }
+            }
         }
     }
     if (advance) {  // this block is the row's only one
@@ -148,17 +158,6 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The row's pairs before the call's eviction (a step's new pair among them), or
-// -1 for a row that is skipped (*bad: and reported).  Block-wide.
-__device__ __forceinline__ int64_t evict_pairs(const EvictParams &p, bool step, int b, int64_t clock, bool &bad) {
-    const int64_t held = p.c.len[b], n = held + (step ? 1 : 0);
-    bad = false;
-    if (held < 0) return -1;
-    bad = held > p.c.capacity() || n > p.c.capacity() || (step && (clock < 0 || clock >= (int64_t(1) << 31)));
-    if (!bad) bad = !block_pages_ok(p.c, b, 0, n - 1);
-    return bad ? -1 : n;
-}
-
 // ---- at most one pair leaves (the steady state; the step's first kernel) ----------
 //
 // The slice of A comes in by one bulk copy while the weights are looked
@@ -168,14 +167,15 @@ __device__ __forceinline__ int64_t evict_pairs(const EvictParams &p, bool step, 
 constexpr int kOneThreads = 256;
 constexpr int kOneWarps = kOneThreads / 32;
 constexpr int kQBatch = 4;    // query heads per pass over A
-constexpr int kScanBatch = 4; // weights in flight per thread
+constexpr int kScanBatch = 8; // weights in flight per thread
 
 template <typename T, int D, bool STEP>
-__global__ void __launch_bounds__(kOneThreads) evict_one_kernel(const __grid_constant__ EvictParams p, int slices) {
+__global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_constant__ EvictParams p, int slices) {
     constexpr int CG = D / 4;              // float4 columns of A
     constexpr int RG = kOneThreads / CG;   // rows of A side by side
     extern __shared__ __align__(128) unsigned char dyn[];
-    __shared__ __align__(16) float s_k[D], s_v[D];
+    __shared__ __align__(16) float s_k[D], s_v[D];            // the pair that leaves
+    __shared__ __align__(16) T s_new[2][D];                   // the new pair
     __shared__ float s_cos[D / 2 + 1], s_sin[D / 2 + 1];
     __shared__ uint64_t s_key[kOneWarps];
     __shared__ uint32_t s_slot[kOneWarps];
@@ -189,14 +189,34 @@ __global__ void __launch_bounds__(kOneThreads) evict_one_kernel(const __grid_con
     const int rank = blockIdx.x % slices;
     const int64_t bh = blockIdx.x / slices;
     const int b = (int)(bh / c.H), h = (int)(bh % c.H);
-    const int64_t clock0 = c.clock[b];
+    const int64_t held = c.len[b], clock0 = c.clock[b];
+    const int G = STEP ? p.Hq / c.H : 0;
     const bool first = h == 0 && rank == 0 && tid == 0;
     const int rows = D / slices, row0 = rank * rows;
     const bool read = STEP && p.memo != nullptr;
     float4 *A4 = c.A ? reinterpret_cast<float4 *>(c.A + (bh * D + row0) * D) : nullptr;
     float4 *sA = reinterpret_cast<float4 *>(dyn);
-    const int64_t expect = c.len[b] + (STEP ? 1 : 0);
-    const bool copy = A4 && expect >= 0 && (read || expect > p.budget) && (STEP || expect - p.budget == 1);
+
+    // the new token's rows do not wait for the length
+    constexpr int NEW = (2 * D + kOneThreads - 1) / kOneThreads;
+    float fresh[NEW];
+    if (STEP) {
+#pragma unroll
+        for (int i = 0; i < NEW; ++i) {
+            const int x = tid + i * kOneThreads;
+            if (x < 2 * D)
+                fresh[i] = to_f32(x < D ? reinterpret_cast<const T *>(p.k_new)[b * p.ks[0] + h * p.ks[1] + x]
+                                        : reinterpret_cast<const T *>(p.v_new)[b * p.vs[0] + h * p.vs[1] + x - D]);
+        }
+        for (int i = tid; i < p.table.rot / 2; i += kOneThreads)
+            rotary_angle(clock0, p.table.inc[i], p.table.gain, s_cos[i], s_sin[i]);
+    }
+    const int64_t n64 = held < 0 ? -1 : held + (STEP ? 1 : 0);
+    // a step lets one pair leave at most: a row above its budget stays above
+    const int64_t over = n64 - p.budget;
+    const int m = over <= 0 ? 0 : STEP ? 1 : over == 1 ? 1 : 0;
+    bool ok = held >= 0 && n64 <= c.capacity() && held <= c.capacity() && (!STEP || (clock0 >= 0 && clock0 < (int64_t(1) << 31)));
+    const bool copy = A4 && ok && (read || m == 1);
     if (tid == 0) {
         s_abort = 0;
         sm100::mbar_init(&s_bar, 1);
@@ -209,60 +229,81 @@ __global__ void __launch_bounds__(kOneThreads) evict_one_kernel(const __grid_con
                          : "memory");
         }
     }
-    bool bad;
-    const int64_t n64 = evict_pairs(p, STEP, b, clock0, bad);  // its barrier also publishes s_bar
-    // a step lets one pair leave at most: a row above its budget stays above
-    const int64_t over = n64 - p.budget;
-    const int m = over <= 0 ? 0 : STEP ? 1 : over == 1 ? 1 : 0;
-    const int n = (int)n64, keep = n - m;
+    const bool in_range = ok;
+    if (ok) ok = block_pages_ok(c, b, 0, n64 - 1);  // its barrier also publishes s_bar, s_cos, s_sin
     if (first) {
-        if (bad) report(c.status, TC_ERR_DEVICE_BOUNDS);
-        p.row_len[b] = n64 < 0 ? -1 : STEP ? keep : n64;
+        if (held >= 0 && !ok) report(c.status, TC_ERR_DEVICE_BOUNDS);
+        p.row_len[b] = !ok ? -1 : STEP ? n64 - m : n64;
     }
-    if (n64 < 0 || (m == 0 && !STEP)) {
-        if (copy && tid == 0) sm100::mbar_wait_drain(&s_bar, 0);
+    if (!ok || (m == 0 && !STEP)) {
+        if (copy && in_range && tid == 0) sm100::mbar_wait_drain(&s_bar, 0);
         return;  // the whole cluster
     }
+    const int n = (int)n64, keep = n - m;
     const int32_t *table = c.table + (int64_t)b * c.max_pages;
     auto row_of = [&](int slot) {
         const int pg = c.page_of(slot);
         return pool_row(c, table[pg], h, slot - pg * c.page);
     };
     T *kp = reinterpret_cast<T *>(c.k), *vp = reinterpret_cast<T *>(c.v);
-    const int G = STEP ? p.Hq / c.H : 0;
+
+    // weights and positions of the pairs held before: under way while the new pair enters
+    const int seen = STEP ? n - 1 : n;
+    float w[kScanBatch];
+    int32_t z[kScanBatch];
+    auto look = [&](int s0) {
+#pragma unroll
+        for (int i = 0; i < kScanBatch; ++i) {
+            const int s = s0 + i * kOneThreads;
+            if (s < seen) {
+                const int64_t row = row_of(s);
+                w[i] = c.mass[row];
+                z[i] = c.pos[row];
+            }
+        }
+    };
+    if (m == 1) look(tid);
 
     if (STEP) {
         // the new pair enters slot n - 1 (every block of the cluster writes the
         // same values), the queries are rotated
         const RotaryTable &rt = p.table;
-        for (int i = tid; i < rt.rot / 2; i += kOneThreads) rotary_angle(clock0, rt.inc[i], rt.gain, s_cos[i], s_sin[i]);
-        __syncthreads();
+        const int half = rt.rot / 2;
+        auto turned = [&](float f, float g, int i) {  // element i, its pair's other element g
+            const int pair = rt.interleaved ? i / 2 : i < half ? i : i - half;
+            const bool second = rt.interleaved ? (i & 1) : i >= half;
+            return second ? g * s_sin[pair] + f * s_cos[pair] : f * s_cos[pair] - g * s_sin[pair];
+        };
+        auto other = [&](int i) { return rt.interleaved ? i ^ 1 : i < half ? i + half : i - half; };
         const int64_t row = row_of(n - 1);
-        for (int x = tid; x < (G + 2) * D; x += kOneThreads) {
-            const int which = x / D, i = x % D;
-            if (which == G + 1) {
-                vp[row * D + i] = reinterpret_cast<const T *>(p.v_new)[b * p.vs[0] + h * p.vs[1] + i];
-                continue;
-            }
-            const T *src = which == G ? reinterpret_cast<const T *>(p.k_new) + b * p.ks[0] + h * p.ks[1]
-                                      : reinterpret_cast<const T *>(p.q) + b * p.qs[0] + (h * G + which) * p.qs[1];
+#pragma unroll
+        for (int i = 0; i < NEW; ++i) {
+            const int x = tid + i * kOneThreads;
+            if (x < D) s_k[x] = fresh[i];
+            else if (x < 2 * D) s_new[1][x - D] = from_f32<T>(fresh[i]);
+        }
+        __syncthreads();
+        for (int x = tid; x < D; x += kOneThreads)
+            s_new[0][x] = from_f32<T>(x < rt.rot ? turned(s_k[x], s_k[other(x)], x) : s_k[x]);
+        for (int x = tid; x < G * D; x += kOneThreads) {
+            const int g = x / D, i = x % D;
+            const T *src = reinterpret_cast<const T *>(p.q) + b * p.qs[0] + (h * G + g) * p.qs[1];
             float f = to_f32(src[i]);
-            if (i < rt.rot) {
-                const int half = rt.rot / 2;
-                const int pair = rt.interleaved ? i / 2 : i < half ? i : i - half;
-                const bool second = rt.interleaved ? (i & 1) : i >= half;
-                const int other = rt.interleaved ? i ^ 1 : (second ? i - half : i + half);
-                const float g = to_f32(src[other]);
-                f = second ? g * s_sin[pair] + f * s_cos[pair] : f * s_cos[pair] - g * s_sin[pair];
-            }
-            if (which == G) kp[row * D + i] = from_f32<T>(f);
-            else reinterpret_cast<T *>(p.q_rot)[(bh * G + which) * D + i] = from_f32<T>(f);
+            if (i < rt.rot) f = turned(f, to_f32(src[other(i)]), i);
+            const T r = from_f32<T>(f);
+            if (rank == 0) reinterpret_cast<T *>(p.q_rot)[(bh * G + g) * D + i] = r;
+            if (g < kQBatch) s_q[g][i] = to_f32(r);  // the first batch's; later ones are rotated again
+        }
+        __syncthreads();
+        constexpr int LPR = D * (int)sizeof(T) / 16;  // 16-byte vectors of a row
+        if (tid < 2 * LPR) {
+            const int i = tid < LPR ? tid : tid - LPR;
+            reinterpret_cast<uint4 *>((tid < LPR ? kp : vp) + row * D)[i] = reinterpret_cast<const uint4 *>(s_new[tid < LPR ? 0 : 1])[i];
         }
         if (tid == 0) {
             c.mass[row] = 0.f;
             c.pos[row] = (int32_t)clock0;
         }
-        __syncthreads();
     }
 
     int gone = 0;  // the slot that leaves
@@ -270,28 +311,27 @@ __global__ void __launch_bounds__(kOneThreads) evict_one_kernel(const __grid_con
         const int64_t protect_from = clock0 + (STEP ? 1 : 0) - p.recent;
         uint64_t best = ~0ull;
         uint32_t slot = 0xffffffffu;
-        for (int s0 = tid; s0 < n; s0 += kScanBatch * kOneThreads) {
-            float w[kScanBatch];
-            int32_t z[kScanBatch];
+        for (int s0 = tid;;) {
 #pragma unroll
             for (int i = 0; i < kScanBatch; ++i) {
                 const int s = s0 + i * kOneThreads;
-                if (s < n) {
-                    const int64_t row = row_of(s);
-                    w[i] = c.mass[row];
-                    z[i] = c.pos[row];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kScanBatch; ++i) {
-                const int s = s0 + i * kOneThreads;
-                if (s < n) {
+                if (s < seen) {
                     const uint64_t key = leave_key(w[i], z[i], protect_from);
                     if (less_pair(key, (uint32_t)s, best, slot)) {
                         best = key;
                         slot = (uint32_t)s;
                     }
                 }
+            }
+            s0 += kScanBatch * kOneThreads;
+            if (s0 >= seen) break;
+            look(s0);
+        }
+        if (STEP && tid == 0) {
+            const uint64_t key = leave_key(0.f, (int32_t)clock0, protect_from);
+            if (less_pair(key, (uint32_t)(n - 1), best, slot)) {
+                best = key;
+                slot = (uint32_t)(n - 1);
             }
         }
 #pragma unroll
@@ -309,33 +349,51 @@ __global__ void __launch_bounds__(kOneThreads) evict_one_kernel(const __grid_con
         }
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kOneWarps; ++w)
-            if (w == 0 || less_pair(s_key[w], s_slot[w], best, slot)) {
-                best = s_key[w];
-                slot = s_slot[w];
+        for (int x = 0; x < kOneWarps; ++x)
+            if (x == 0 || less_pair(s_key[x], s_slot[x], best, slot)) {
+                best = s_key[x];
+                slot = s_slot[x];
             }
         gone = (int)slot;
     }
 
     if (copy) {
-        const int cg = tid % CG, rg = tid / CG;
-        const float lam = c.lam[h], eta = c.eta[h];
         if (m == 1) {
-            const int64_t row = row_of(gone);
+            const bool is_new = STEP && gone == n - 1;
+            const int64_t row = is_new ? 0 : row_of(gone);
             for (int i = tid; i < 2 * D; i += kOneThreads) {
-                if (i < D) s_k[i] = to_f32(kp[row * D + i]);
-                else s_v[i - D] = to_f32(vp[row * D + i - D]);
+                const bool value = i >= D;
+                const int e = value ? i - D : i;
+                const T x = is_new ? s_new[value][e] : (value ? vp : kp)[row * D + e];
+                if (value) s_v[e] = to_f32(x);
+                else s_k[e] = to_f32(x);
             }
         }
         if (!sm100::mbar_wait(&s_bar, 0, &s_abort, c.status, p.wait_ns)) sm100::mbar_wait_drain(&s_bar, 0);
         __syncthreads();
+    }
+    // every block of the cluster that gets here has read the pair that leaves:
+    // the barrier is waited for where its slot is written
+    if (m == 1 && slices > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (copy) {
+        const int cg = tid % CG, rg = tid / CG;
+        const float lam = c.lam[h], eta = c.eta[h];
         const float4 v4 = m == 1 ? reinterpret_cast<const float4 *>(s_v)[cg] : make_float4(0.f, 0.f, 0.f, 0.f);
         for (int g0 = 0; g0 == 0 || g0 < G; g0 += kQBatch) {
             const int ng = read ? min(kQBatch, G - g0) : 0;
-            if (read) {
-                for (int x = tid; x < kQBatch * rows; x += kOneThreads) {
-                    const int g = x / rows, r = x - g * rows;
-                    s_q[g][r] = g < ng ? to_f32(reinterpret_cast<const T *>(p.q_rot)[(bh * G + g0 + g) * D + row0 + r]) : 0.f;
+            if (g0 > 0) {  // (read) later batches: the queries again
+                for (int x = tid; x < ng * D; x += kOneThreads) {
+                    const int g = x / D, i = x % D;
+                    const T *src = reinterpret_cast<const T *>(p.q) + b * p.qs[0] + (h * G + g0 + g) * p.qs[1];
+                    float f = to_f32(src[i]);
+                    const int half = p.table.rot / 2;
+                    if (i < p.table.rot) {
+                        const int pair = p.table.interleaved ? i / 2 : i < half ? i : i - half;
+                        const bool second = p.table.interleaved ? (i & 1) : i >= half;
+                        const float y = to_f32(src[p.table.interleaved ? i ^ 1 : i < half ? i + half : i - half]);
+                        f = second ? y * s_sin[pair] + f * s_cos[pair] : f * s_cos[pair] - y * s_sin[pair];
+                    }
+                    s_q[g][i] = to_f32(from_f32<T>(f));
                 }
                 __syncthreads();
             }
@@ -357,11 +415,11 @@ __global__ void __launch_bounds__(kOneThreads) evict_one_kernel(const __grid_con
                 if (read) {
 #pragma unroll
                     for (int g = 0; g < kQBatch; ++g) {
-                        const float w = s_q[g][r];
-                        mp[g].x = fmaf(w, a.x, mp[g].x);
-                        mp[g].y = fmaf(w, a.y, mp[g].y);
-                        mp[g].z = fmaf(w, a.z, mp[g].z);
-                        mp[g].w = fmaf(w, a.w, mp[g].w);
+                        const float x = s_q[g][row0 + r];  // heads past the last: never stored
+                        mp[g].x = fmaf(x, a.x, mp[g].x);
+                        mp[g].y = fmaf(x, a.y, mp[g].y);
+                        mp[g].z = fmaf(x, a.z, mp[g].z);
+                        mp[g].w = fmaf(x, a.w, mp[g].w);
                     }
                 }
             }
@@ -381,29 +439,29 @@ __global__ void __launch_bounds__(kOneThreads) evict_one_kernel(const __grid_con
     }
     if (m == 0) return;  // the whole cluster
 
-    // the last pair moves to the freed slot, once every block of the cluster has
-    // read what that overwrites
-    if (slices > 1) cluster_sync();
+    // the last pair moves to the freed slot (a step's: the new one, from here)
+    if (slices > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     else __syncthreads();
-    constexpr int LPR = D * (int)sizeof(T) / 16;  // 16-byte vectors of a row
+    constexpr int LPR = D * (int)sizeof(T) / 16;
     if (rank == 0 && gone < keep && tid < 2 * LPR) {
         const int64_t from = row_of(keep), to = row_of(gone);
         T *pool = tid < LPR ? kp : vp;
         const int i = tid < LPR ? tid : tid - LPR;
-        reinterpret_cast<uint4 *>(pool + to * D)[i] = reinterpret_cast<const uint4 *>(pool + from * D)[i];
+        reinterpret_cast<uint4 *>(pool + to * D)[i] = STEP ? reinterpret_cast<const uint4 *>(s_new[tid < LPR ? 0 : 1])[i]
+                                                           : reinterpret_cast<const uint4 *>(pool + from * D)[i];
         if (tid == 0) {
-            c.mass[to] = c.mass[from];
-            c.pos[to] = c.pos[from];
+            c.mass[to] = STEP ? 0.f : c.mass[from];
+            c.pos[to] = STEP ? (int32_t)clock0 : c.pos[from];
         }
     }
 }
 
 // ---- several pairs leave ------------------------------------------------------------
 //
-// The slots are sorted by (protected, mass, pos) with a stable radix sort of 8
-// bits a pass, in shared memory up to kSortMax pairs; passes whose digit is the
-// same for every pair (most of the positions' and the protection's) are skipped.
-// (A bitonic sort of 4096 keys with their slots took 139,000 cycles.)  The
+// The slots are sorted by (protected, mass, pos) with a stable radix sort, in
+// shared memory up to kSortMax pairs, over the bits in which pairs differ.  (2559
+// pairs: a bitonic sort of the keys took 139,000 cycles, 8 bits a pass with a
+// warp's lanes matched against one another 82,000, 4 bits as below 41,000.)  The
 // weighted sum runs on the tensor cores: tiles of TP pairs come in by
 // asynchronous 16-byte copies, several in flight; the weighted keys
 // lambda^(m-1-i) k_i are split into three bf16 parts (24 bits together; a
@@ -455,55 +513,140 @@ __device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
     return before + v - x;
 }
 
-// One stable pass of 8 bits: order b of n slots from order a by (key[slot] >>
-// shift) & 255.  Each warp counts the digits of its share, the counts' prefix
-// over (digit, warp) gives every element its place.  False (and b untouched)
-// when all digits are the same.
-__device__ bool radix_pass(const uint32_t *key, const uint32_t *a, uint32_t *b, int n, int shift, uint32_t *counts, int *scan) {
+// One stable pass over a digit: order b of n slots from order a by the bits of
+// key[slot] from `shift` on.  A thread takes ITEMS consecutive places (an odd
+// number, so that the lanes' reads fall into different banks) and counts its
+// digits in counters of its own, [digit][thread]; a warp per row of counters
+// makes their prefix; the counters then give every element its place.  Counters
+// of 16 bits, two digits a row, make 5 bits a pass; ITEMS 0 (any number of
+// pairs, each read twice) needs 32 and takes 4.  The counters are the thread's
+// own, so the atomic additions meet nobody: they are used because they do not
+// wait for one another as loads and stores would.
+template <int ITEMS>
+struct RadixDigit {
+    static constexpr int BITS = ITEMS ? 5 : 4;
+    static constexpr uint32_t MASK = (1u << BITS) - 1u;
+    __device__ __forceinline__ static uint32_t row(uint32_t d) { return ITEMS ? d >> 1 : d; }
+    __device__ __forceinline__ static uint32_t one(uint32_t d) { return ITEMS ? 1u << ((d & 1u) * 16) : 1u; }
+    __device__ __forceinline__ static uint32_t count(uint32_t word, uint32_t d) { return ITEMS ? (word >> ((d & 1u) * 16)) & 0xffffu : word; }
+};
+
+template <int ITEMS>
+__device__ __forceinline__ void radix_pass(const uint32_t *key, const uint32_t *a, uint32_t *b, int n, int shift, uint32_t *counts,
+                                           uint32_t *total, uint32_t (*base)[32]) {
+    using R = RadixDigit<ITEMS>;
+    static_assert(kBulkWarps == 16, "a warp per row of counters");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int share = (n + kBulkWarps * 32 - 1) / (kBulkWarps * 32) * 32, i0 = warp * share, i1 = min(n, i0 + share);
-    uint32_t *mine = counts + warp * 256;
-    __syncthreads();
-    for (int x = tid; x < kBulkWarps * 256; x += kBulkThreads) counts[x] = 0;
-    __syncthreads();
-    for (int i = i0 + lane; i < i0 + share; i += 32) {
-        const uint32_t d = i < i1 ? (key[a[i]] >> shift) & 255u : 256u;
-        const uint32_t same = __match_any_sync(0xffffffffu, d);
-        if (d < 256u && (same & ((1u << lane) - 1u)) == 0) mine[d] += __popc(same);
-        __syncwarp();
+    const int per = ITEMS ? ITEMS : ((n + kBulkThreads - 1) / kBulkThreads) | 1, i0 = min(n, tid * per), i1 = min(n, i0 + per);
+    uint32_t *mine = counts + tid;
+#pragma unroll
+    for (int d = 0; d < 16; ++d) mine[d * kBulkThreads] = 0;
+    uint32_t s[ITEMS ? ITEMS : 1], digit[ITEMS ? ITEMS : 1];
+    if (ITEMS) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) s[i] = i0 + i < i1 ? a[i0 + i] : 0u;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) digit[i] = (key[s[i]] >> shift) & R::MASK;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (i0 + i < i1) mine[R::row(digit[i]) * kBulkThreads] += R::one(digit[i]);
+    } else {
+        for (int i = i0; i < i1; ++i) atomicAdd(mine + ((key[a[i]] >> shift) & R::MASK) * kBulkThreads, 1u);
     }
     __syncthreads();
-    int sum = 0, total;
-    if (tid < 256) {
+    uint4 *row = reinterpret_cast<uint4 *>(counts + warp * kBulkThreads);
+    uint4 c[kBulkThreads / 128];
+    uint32_t v[kBulkThreads / 128];
 #pragma unroll
-        for (int w = 0; w < kBulkWarps; ++w) sum += counts[w * 256 + tid];
+    for (int x = 0; x < kBulkThreads / 128; ++x) {
+        c[x] = row[x * 32 + lane];
+        v[x] = c[x].x + c[x].y + c[x].z + c[x].w;
     }
-    if (__syncthreads_or(sum == n)) return false;
-    int at = block_scan(sum, scan, &total);
-    if (tid < 256) {
 #pragma unroll
-        for (int w = 0; w < kBulkWarps; ++w) {
-            const int c = (int)counts[w * 256 + tid];
-            counts[w * 256 + tid] = (uint32_t)at;
-            at += c;
+    for (int o = 1; o < 32; o *= 2)
+#pragma unroll
+        for (int x = 0; x < kBulkThreads / 128; ++x) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, v[x], o);
+            if (lane >= o) v[x] += y;
+        }
+    uint32_t before = 0;
+#pragma unroll
+    for (int x = 0; x < kBulkThreads / 128; ++x) {
+        const uint32_t p = before + v[x] - (c[x].x + c[x].y + c[x].z + c[x].w);
+        row[x * 32 + lane] = make_uint4(p, p + c[x].x, p + c[x].x + c[x].y, p + c[x].x + c[x].y + c[x].z);
+        before += __shfl_sync(0xffffffffu, v[x], 31);
+    }
+    if (lane == 0) {
+        if (ITEMS) {
+            total[2 * warp] = before & 0xffffu;
+            total[2 * warp + 1] = before >> 16;
+        } else {
+            total[warp] = before;
         }
     }
     __syncthreads();
-    for (int i = i0 + lane; i < i0 + share; i += 32) {
-        const uint32_t s = i < i1 ? a[i] : 0u;
-        const uint32_t d = i < i1 ? (key[s] >> shift) & 255u : 256u;
-        const uint32_t same = __match_any_sync(0xffffffffu, d);
-        const uint32_t before = __popc(same & ((1u << lane) - 1u));
-        const uint32_t base = d < 256u ? mine[d] : 0u;
-        __syncwarp();
-        if (d < 256u) {
-            b[base + before] = s;
-            if (before == 0) mine[d] = base + __popc(same);
+    {  // where each digit begins, a copy per warp
+        const uint32_t x = lane <= (int)R::MASK ? total[lane] : 0u;
+        uint32_t sum = x;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
         }
+        base[warp][lane] = sum - x;
         __syncwarp();
     }
+    if (ITEMS) {
+        uint32_t to[ITEMS ? ITEMS : 1];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (i0 + i < i1) {
+                uint32_t &word = mine[R::row(digit[i]) * kBulkThreads];
+                const uint32_t old = word;
+                word = old + R::one(digit[i]);
+                to[i] = R::count(old, digit[i]);
+            }
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (i0 + i < i1) b[to[i] + base[warp][digit[i]]] = s[i];
+    } else {
+        for (int i = i0; i < i1; ++i) {
+            const uint32_t x = a[i], d = (key[x] >> shift) & R::MASK;
+            b[atomicAdd(mine + d * kBulkThreads, 1u) + base[warp][d]] = x;
+        }
+    }
     __syncthreads();
-    return true;
+}
+
+// Sorts the slots 0 .. n-1 by (place, then weight, then place's bit 31), least
+// significant first; only the digits in which pairs differ take a pass.  The
+// protection (bit 31) rides along in the position's last pass and changes
+// nothing there: it is the last criterion again.  Returns where the order is.
+template <int ITEMS>
+__device__ __forceinline__ uint32_t *sort_slots(uint32_t *order, uint32_t *other, const uint32_t *weight, uint32_t *place, int n,
+                                                bool by_place, uint32_t w_differ, uint32_t z_differ, uint32_t *counts,
+                                                uint32_t *total, uint32_t (*base)[32]) {
+    using R = RadixDigit<ITEMS>;
+    bool swapped = false;
+    auto pass = [&](const uint32_t *key, int shift) {
+        radix_pass<ITEMS>(key, swapped ? other : order, swapped ? order : other, n, shift, counts, total, base);
+        swapped = !swapped;
+    };
+    // digits begin at the lowest bit in which pairs differ
+    for (int part = by_place ? 0 : 1; part < 2; ++part) {
+        uint32_t left = part ? w_differ : z_differ;
+        while (left) {
+            const int shift = __ffs(left) - 1;
+            pass(part ? weight : place, shift);
+            left = shift + R::BITS < 32 ? left >> (shift + R::BITS) << (shift + R::BITS) : 0u;
+        }
+    }
+    if (z_differ >> 31) {
+        for (int s = threadIdx.x; s < n; s += kBulkThreads) place[s] >>= 31;
+        __syncthreads();
+        pass(place, 0);
+    }
+    return swapped ? other : order;
 }
 
 __device__ __forceinline__ void ldsm_t4(const void *p, uint32_t (&r)[4]) {
@@ -529,14 +672,19 @@ __device__ __forceinline__ void copy16(void *dst, const void *src) {
 }
 __device__ __forceinline__ void zero16(void *dst) { *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0); }
 
-// x, y as three bf16 pairs whose sum is exact to 24 bits.
+// x, y as three bf16 pairs whose sum is x, y: eight leading bits at a time, cut
+// off and not rounded, so that 24 bits take three and nothing overflows.
 __device__ __forceinline__ void split3(float x, float y, uint32_t (&o)[3]) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        o[i] = pack_bf16_rn(x, y);
-        const float hx = __uint_as_float(o[i] << 16), hy = __uint_as_float(o[i] & 0xffff0000u);
-        x = isinf(hx) ? 0.f : x - hx;  // an infinity has no rest
-        y = isinf(hy) ? 0.f : y - hy;
+        const uint32_t hx = __float_as_uint(x) & 0xffff0000u, hy = __float_as_uint(y) & 0xffff0000u;
+        o[i] = __byte_perm(hx, hy, 0x7632);
+        x -= __uint_as_float(hx);
+        y -= __uint_as_float(hy);
+        if (i == 0) {  // an infinity (or NaN) has no rest
+            x = x == x ? x : 0.f;
+            y = y == y ? y : 0.f;
+        }
     }
 }
 
@@ -558,21 +706,23 @@ struct BulkShape {
     // output tiles of 16 x 8: warps along the rows first
     static constexpr int TM = D / 16, TN = D / 8, NWN = kBulkWarps / TM;
     static constexpr int NT = TN / NWN > 0 ? TN / NWN : 1;  // tiles a warp holds
+    static_assert(kSortMax <= 17 * kBulkThreads, "sorted in registers");
     static_assert(SUM >= 4 * D * D, "the block's sum has to fit");
 };
 
 // Bytes of sorting room for up to n pairs (a multiple of 32): keys, positions,
-// second order; with the counts, and the first order, which stays.
-__host__ __device__ constexpr size_t sort_room(size_t n) { return 12 * n + kBulkWarps * 256 * 4; }
-__host__ __device__ constexpr size_t order_room(size_t n) { return (4 * n + n / 8 + 127) / 128 * 128; }  // and a bit per slot
+// second order; and the counts.
+__host__ __device__ constexpr size_t sort_room(size_t n) { return 12 * n + 16 * kBulkThreads * 4; }
+// What stays through all of it: the order (later the pairs' pool rows), the
+// weights in the sum, a bit per slot.
+__host__ __device__ constexpr size_t order_room(size_t n) { return (8 * n + n / 8 + 127) / 128 * 128; }
 
 template <typename T, int D, int SL>
-__global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_constant__ EvictParams p, int n_cap) {
+__global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kernel(const __grid_constant__ EvictParams p, int n_cap) {
     using S = BulkShape<T, D>;
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ int s_scan[kBulkWarps];
-    __shared__ int s_row[S::STAGES + 1][S::TP];
-    __shared__ float s_w[S::STAGES + 1][S::TP];
+    __shared__ uint32_t s_total[32], s_base[kBulkWarps][32], s_bits[4][kBulkWarps];
 
     const CacheParams &c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -594,19 +744,20 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_c
 
     // ---- the order of leaving -----------------------------------------------------
     const bool inside = n <= n_cap;
-    const size_t room = inside ? n_cap : n2_cap_global(c.capacity());
+    const size_t room = inside ? n_cap : pairs_room(c.capacity());
     unsigned char *kept = inside ? dyn : p.sort_ws + (bh * SL + rank) * (order_room(room) + sort_room(room));
     unsigned char *scratch = kept + order_room(room);     // sorting and lists
     unsigned char *tiles_mem = dyn + order_room(n_cap);   // the sum
-    uint32_t *order = reinterpret_cast<uint32_t *>(kept), *bits = order + room;
+    uint32_t *order = reinterpret_cast<uint32_t *>(kept), *bits = order + 2 * room;
+    float *factor = reinterpret_cast<float *>(order + room);
     uint32_t *weight = reinterpret_cast<uint32_t *>(scratch), *place = weight + room, *other = place + room;
     uint32_t *counts = other + room;
     const int words = (n + 31) / 32;
     {
         const int64_t protect_from = c.clock[b] - p.recent;
         bool sorted = true;  // by position already, as tokens are appended
-        uint32_t prot_any = 0, prot_all = 1;
-        constexpr int U = 4;
+        uint32_t w_or = 0, w_and = ~0u, z_or = 0, z_and = ~0u;  // bits that differ between pairs
+        constexpr int U = 8;
         for (int s0 = tid; s0 < n; s0 += U * kBulkThreads) {
             float w[U];
             int32_t z[U];
@@ -628,8 +779,10 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_c
                     // the position, and above it the protection
                     place[s] = (uint32_t)(key & 0x7fffffffu) | (uint32_t)(key >> 63) << 31;
                     order[s] = s;
-                    prot_any |= (uint32_t)(key >> 63);
-                    prot_all &= (uint32_t)(key >> 63);
+                    w_or |= weight[s];
+                    w_and &= weight[s];
+                    z_or |= place[s];
+                    z_and &= place[s];
                 }
             }
         }
@@ -638,30 +791,55 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_c
         for (int s = tid; s + 1 < n; s += kBulkThreads)
             sorted = sorted && (place[s] & 0x7fffffffu) <= (place[s + 1] & 0x7fffffffu);
         const bool by_place = !__syncthreads_and(sorted);
-        const bool split = __syncthreads_or(prot_any) && !__syncthreads_and(prot_all);
-        uint32_t *from = order, *to = other;
-        auto pass = [&](const uint32_t *key, int shift) {
-            if (radix_pass(key, from, to, n, shift, counts, s_scan)) {
-                uint32_t *x = from;
-                from = to;
-                to = x;
-            }
-        };
-        // least significant first.  (The protection rides in the positions' top
-        // digit, which changes nothing: it is the last criterion again.)
-        if (by_place)
-            for (int shift = 0; shift < 32; shift += 8) pass(place, shift);
-        for (int shift = 0; shift < 32; shift += 8) pass(weight, shift);
-        if (split) pass(place, 31);
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) {
+            w_or |= __shfl_xor_sync(0xffffffffu, w_or, o);
+            w_and &= __shfl_xor_sync(0xffffffffu, w_and, o);
+            z_or |= __shfl_xor_sync(0xffffffffu, z_or, o);
+            z_and &= __shfl_xor_sync(0xffffffffu, z_and, o);
+        }
+        if (lane == 0) {
+            s_bits[0][warp] = w_or;
+            s_bits[1][warp] = ~w_and;
+            s_bits[2][warp] = z_or;
+            s_bits[3][warp] = ~z_and;
+        }
         __syncthreads();
-        if (from != order)
-            for (int i = tid; i < n; i += kBulkThreads) order[i] = from[i];
+        uint32_t differ[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < kBulkWarps; ++w)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) differ[i] |= s_bits[i][w];
+        const uint32_t w_differ = differ[0] & differ[1], z_differ = differ[2] & differ[3];
+        const uint32_t *from;
+        if (inside) {
+            // the same addresses, from the block's own shared memory, so that they
+            // are accessed as such
+            uint32_t *o = reinterpret_cast<uint32_t *>(dyn), *w = reinterpret_cast<uint32_t *>(dyn + order_room(n_cap));
+            auto sort = [&](auto items) {
+                return sort_slots<decltype(items)::value>(o, w + 2 * n_cap, w, w + n_cap, n, by_place, w_differ, z_differ, w + 3 * n_cap, s_total, s_base);
+            };
+            from = n <= kBulkThreads       ? sort(std::integral_constant<int, 1>())
+                   : n <= 3 * kBulkThreads ? sort(std::integral_constant<int, 3>())
+                   : n <= 5 * kBulkThreads ? sort(std::integral_constant<int, 5>())
+                   : n <= 9 * kBulkThreads ? sort(std::integral_constant<int, 9>())
+                                           : sort(std::integral_constant<int, 17>());
+        } else {
+            from = sort_slots<0>(order, other, weight, place, n, by_place, w_differ, z_differ, counts, s_total, s_base);
+        }
+        // the pairs that leave: marked, and from here on named by their pool rows
+        const Decay decay(c.A ? c.lam[h] : 1.f);
+        for (int i = tid; i < m; i += kBulkThreads) {
+            const uint32_t s = from[i];
+            atomicOr(&bits[s / 32], 1u << (s % 32));
+            order[i] = (uint32_t)row_of((int)s);
+            factor[i] = decay.pow(m - 1 - i);
+        }
         __syncthreads();
     }
 
     // ---- A: lambda^m A + eta sum of lambda^(m-1-i) k_i v_i^T -------------------------
     if (c.A) {
-        const Decay decay(c.lam[h]);
         unsigned char *parts = tiles_mem + S::STAGES * S::RAW;
         const int wm = warp % S::TM, wn = (warp / S::TM) * S::NT;
         const bool works = wn < S::TN;
@@ -671,21 +849,14 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_c
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[t][e] = 0.f;
         const int all = (m + S::TP - 1) / S::TP, tiles = (all - rank + SL - 1) / SL;  // every SL-th is this block's
-        // pool rows and weights of a tile's pairs
-        auto plan = [&](int tile) {
-            if (tid < S::TP && tile < tiles) {
-                const int i = (tile * SL + rank) * S::TP + tid;
-                s_row[tile % (S::STAGES + 1)][tid] = i < m ? row_of((int)order[i]) : -1;
-                s_w[tile % (S::STAGES + 1)][tid] = i < m ? decay.pow(m - 1 - i) : 0.f;
-            }
-        };
         auto fetch = [&](int tile) {
             if (tile < tiles) {
                 unsigned char *raw = tiles_mem + (tile % S::STAGES) * S::RAW;
                 constexpr int RC = D * (int)sizeof(T) / 16, EL = 16 / (int)sizeof(T);  // chunks of a row, elements of one
                 for (int x = tid; x < S::TP * 2 * RC; x += kBulkThreads) {
                     const int pr = x / (2 * RC), ch = x % (2 * RC);
-                    const int64_t row = s_row[tile % (S::STAGES + 1)][pr];
+                    const int i = (tile * SL + rank) * S::TP + pr;
+                    const int64_t row = i < m ? (int64_t)order[i] : -1;
                     unsigned char *dst = ch < RC ? raw + pr * S::KRAW + ch * 16 : raw + S::TP * S::KRAW + pr * S::VRAW + (ch - RC) * 16;
                     const T *src = ch < RC ? kp + row * D + ch * EL : vp + row * D + (ch - RC) * EL;
                     if (row >= 0) copy16(dst, src);
@@ -694,29 +865,29 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_c
             }
             asm volatile("cp.async.commit_group;" ::: "memory");  // an empty group past the last tile
         };
-        for (int i = 0; i < S::STAGES; ++i) plan(i);
-        __syncthreads();
         for (int i = 0; i < S::STAGES - 1; ++i) fetch(i);
         for (int tile = 0; tile < tiles; ++tile) {
             asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 2) : "memory");
             __syncthreads();  // the tile is there; the parts and the last tile's buffer are free
             fetch(tile + S::STAGES - 1);
-            plan(tile + S::STAGES);
             const unsigned char *raw = tiles_mem + (tile % S::STAGES) * S::RAW;
-            for (int x = tid; x < S::TP * D / 2; x += kBulkThreads) {
-                const int pr = x / (D / 2), e = x % (D / 2);
-                const T *src = reinterpret_cast<const T *>(raw + pr * S::KRAW) + 2 * e;
-                const float w = s_w[tile % (S::STAGES + 1)][pr];
-                uint32_t o[3];
-                split3(w * to_f32(src[0]), w * to_f32(src[1]), o);
+            for (int x = tid; x < S::TP * D / 8; x += kBulkThreads) {  // eight elements a thread
+                const int pr = x / (D / 8), e = x % (D / 8), i = (tile * SL + rank) * S::TP + pr;
+                const float w = i < m ? factor[i] : 0.f;
+                auto part = [&](const unsigned char *src, float scale, int first) {
+                    float f[8];
+                    uint32_t o[4][3];
 #pragma unroll
-                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(parts + (i * S::TP + pr) * S::PS + e * 4) = o[i];
-                if (S::VPARTS) {
-                    const T *val = reinterpret_cast<const T *>(raw + S::TP * S::KRAW + pr * S::VRAW) + 2 * e;
-                    split3(to_f32(val[0]), to_f32(val[1]), o);
+                    for (int y = 0; y < 8; y += Vec16<T>::N)
+                        Vec16<T>::unpack(reinterpret_cast<const uint4 *>(src + e * 8 * sizeof(T))[y / Vec16<T>::N], f + y);
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(parts + ((3 + i) * S::TP + pr) * S::PS + e * 4) = o[i];
-                }
+                    for (int y = 0; y < 4; ++y) split3(scale * f[2 * y], scale * f[2 * y + 1], o[y]);
+#pragma unroll
+                    for (int y = 0; y < 3; ++y)
+                        *reinterpret_cast<uint4 *>(parts + ((first + y) * S::TP + pr) * S::PS + e * 16) = make_uint4(o[0][y], o[1][y], o[2][y], o[3][y]);
+                };
+                part(raw + pr * S::KRAW, w, 0);
+                if (S::VPARTS) part(raw + S::TP * S::KRAW + pr * S::VRAW, 1.f, 3);
             }
             __syncthreads();
             if (works) {
@@ -751,7 +922,7 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_c
                     for (int e = 0; e < 4; ++e) sum[t][e] += acc[t][e];
             }
         }
-        const float lm = decay.pow(m), eta = c.eta[h];
+        const float lm = Decay(c.lam[h]).pow(m), eta = c.eta[h];
         const int row = wm * 16 + lane / 4, col = (lane % 4) * 2;
         if constexpr (SL == 1) {
             if (works) {
@@ -778,10 +949,8 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_c
                         *reinterpret_cast<float2 *>(mine + (row + e * 4) * D + (wn + t) * 8 + col) = make_float2(sum[t][e], sum[t][e + 1]);
             }
             cluster_sync();
-            // this block's rows of A, from every block's sum
-            constexpr int R = D / SL;
-            for (int x = tid; x < R * D / 4; x += kBulkThreads) {
-                const int at = rank * R * D / 4 + x;
+            // this block's share of A, from every block's sum
+            for (int at = rank * kBulkThreads + tid; at < D * D / 4; at += SL * kBulkThreads) {
                 float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int r = 0; r < SL; ++r) {
@@ -807,7 +976,6 @@ __global__ void __launch_bounds__(kBulkThreads) evict_bulk_kernel(const __grid_c
     }
 
     // ---- freed slots below keep, and the pairs behind it that stay ------------------
-    for (int i = tid; i < m; i += kBulkThreads) atomicOr(&bits[order[i] / 32], 1u << (order[i] % 32));
     __syncthreads();
     int *hole = reinterpret_cast<int *>(scratch), *fill = hole + room;
     const int per = (words + kBulkThreads - 1) / kBulkThreads;
@@ -902,8 +1070,8 @@ cudaError_t launch_one(const EvictParams &p, int slices, cudaStream_t s) {
 
 template <typename T, int D, int SL>
 cudaError_t launch_bulk(const EvictParams &p, cudaStream_t s) {
-    const int64_t cap = n2_cap_global(p.c.capacity());
-    const int n2 = (int)(cap < kSortMax ? cap : kSortMax);
+    const int64_t cap = pairs_room(p.c.capacity());
+    const int n2 = (int)(cap < kSortMax ? cap : kSortMax);  // pairs sorted in shared memory
     const size_t sum = BulkShape<T, D>::SUM, sort = sort_room(n2);
     const size_t smem = order_room(n2) + (sum > sort ? sum : sort);
     cudaError_t e = allow_smem(evict_bulk_kernel<T, D, SL>, smem);
@@ -917,9 +1085,7 @@ template <typename T, int D>
 cudaError_t launch_bulk_sl(const EvictParams &p, int slices, cudaStream_t s) {
     if constexpr (D >= 64)
         if (slices == 4) return launch_bulk<T, D, 4>(p, s);
-    if constexpr (D >= 32)
-        if (slices == 2) return launch_bulk<T, D, 2>(p, s);
-    return launch_bulk<T, D, 1>(p, s);
+    return slices >= 2 ? launch_bulk<T, D, 2>(p, s) : launch_bulk<T, D, 1>(p, s);
 }
 
 template <typename T>
@@ -970,11 +1136,16 @@ cudaError_t launch_cache_append(const AppendParams &p, tc_dtype dtype, cudaStrea
 int evict_slices(int64_t BH, int d, int num_sms) { return slices_for(BH, d, d == 128 ? 2 : 1, 4, num_sms); }
 
 namespace {
-int bulk_slices(int64_t BH, int d, int num_sms) { return slices_for(BH, d, 1, 4, num_sms); }
+// Blocks that share a head's pairs: 1, 2 or 4 (2 for the narrow heads, whose sums
+// are short), while all still run at once: two on an SM up to d = 64, one at 128.
+int bulk_slices(int64_t BH, int d, int num_sms) {
+    const int64_t room = (int64_t)(d <= 64 ? 2 : 1) * num_sms;
+    return BH * 4 <= room && d >= 64 ? 4 : BH * 2 <= room && d >= 32 ? 2 : 1;
+}
 }  // namespace
 
 size_t evict_sort_bytes(int64_t BH, int d, int64_t capacity, int num_sms) {
-    const int64_t n2 = n2_cap_global(capacity);
+    const int64_t n2 = pairs_room(capacity);
     return n2 <= kSortMax ? 0 : (size_t)BH * (size_t)bulk_slices(BH, d, num_sms) * (order_room(n2) + sort_room(n2));
 }
 

@@ -22,12 +22,8 @@ struct CacheParams {
     __device__ __forceinline__ int page_of(int slot) const { return (int)(((uint64_t)slot * page_mul) >> 40); }
 };
 
-// The power of two a row's pairs are sorted in: at least 32, at least capacity.
-__host__ __device__ inline int n2_cap_global(int64_t capacity) {
-    int n2 = 32;
-    while (n2 < capacity) n2 *= 2;
-    return n2;
-}
+// Room for a row's pairs: the capacity in whole words of a bit each.
+__host__ __device__ inline int pairs_room(int64_t capacity) { return (int)((capacity + 31) / 32 * 32); }
 
 // Row (of d elements) of slot s, head h, in the pools: page pg is valid.
 __device__ __forceinline__ int64_t pool_row(const CacheParams &c, int pg, int h, int in_page) {
