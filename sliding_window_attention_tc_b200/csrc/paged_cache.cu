@@ -28,7 +28,7 @@ namespace {
 // ---- insertion ------------------------------------------------------------------
 
 constexpr int kAppThreads = 256;
-constexpr int kAppUnroll = 4;
+constexpr int kAppUnroll = 3;
 
 // Tokens row b appends, or -1 when the row is to be skipped (and not because
 // it is empty: *bad says that an error has to be reported).  Block-wide.
@@ -44,42 +44,45 @@ __device__ __forceinline__ int64_t append_count(const AppendParams &p, int b, in
     return bad ? -1 : n;
 }
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_constant__ AppendParams p, int chunks,
-                                                             int tokens, int tiles, bool advance) {
+template <typename T, int VEC, bool INTER>
+__global__ void __launch_bounds__(kAppThreads, 4) append_kernel(const __grid_constant__ AppendParams p, int chunks,
+                                                                int tokens, int tiles, bool advance) {
     const int b = blockIdx.x / tiles;
     const int64_t t0 = (int64_t)(blockIdx.x % tiles) * tokens;
+    const int H = p.c.H, d = p.d;
+    const int chunk = threadIdx.x % chunks, r = threadIdx.x / chunks;
+    const int hg = r / tokens, HG = kAppThreads / chunks / tokens;
+    const int64_t t = t0 + r % tokens;
+    RotChunk<T, VEC, INTER> rc;
+    rc.place(p.table, chunk, d);
+    // rows: the queries' heads, the keys', the values' (copied); kAppUnroll in
+    // flight, the first of them while the row's length and pages are looked up
+    const int q_rows = p.q ? p.Hq : 0, rows = t < p.T && hg < HG ? q_rows + 2 * H : 0;
+    typename RotChunk<T, VEC, INTER>::Raw u[kAppUnroll], w[kAppUnroll];
+    auto load = [&](int x0) {
+#pragma unroll
+        for (int i = 0; i < kAppUnroll; ++i) {
+            const int x = x0 + i * HG;
+            if (x < rows) {
+                const T *src = x < q_rows       ? reinterpret_cast<const T *>(p.q) + b * p.qs[0] + x * p.qs[1] + t * p.qs[2]
+                               : x < q_rows + H ? reinterpret_cast<const T *>(p.k) + b * p.ks[0] + (x - q_rows) * p.ks[1] + t * p.ks[2]
+                                                : reinterpret_cast<const T *>(p.v) + b * p.vs[0] + (x - q_rows - H) * p.vs[1] + t * p.vs[2];
+                rc.load(src, u[i], w[i]);
+            }
+        }
+    };
+    load(hg);
     int64_t len, clock;
     bool bad;
     const int64_t n = append_count(p, b, len, clock, bad);
     if (bad && threadIdx.x == 0) report(p.c.status, TC_ERR_DEVICE_BOUNDS);
     if (n < 0) return;
-    const int H = p.c.H, d = p.d;
-    const int chunk = threadIdx.x % chunks, r = threadIdx.x / chunks;
-    const int hg = r / tokens, HG = kAppThreads / chunks / tokens;
-    const int64_t t = t0 + r % tokens;
     if (t < n && hg < HG) {
-        const int64_t slot = len + t, position = clock + t;
-        const int pg = p.c.table[(int64_t)b * p.c.max_pages + slot / p.c.page];
-        const int in_page = (int)(slot % p.c.page);
-        RotChunk<VEC> rc;
-        rc.place(p.table, chunk, d);
+        const int slot = (int)(len + t), page = p.c.page_of(slot), in_page = slot - page * p.c.page;
+        const int64_t position = clock + t;
+        const int pg = p.c.table[(int64_t)b * p.c.max_pages + page];
         rc.angles(p.table, chunk, position, false);
-        // rows: the queries' heads, the keys', the values' (copied); kAppUnroll in flight
-        const int q_rows = p.q ? p.Hq : 0, rows = q_rows + 2 * H;
-        for (int x0 = hg; x0 < rows; x0 += kAppUnroll * HG) {
-            float u[kAppUnroll][VEC], w[kAppUnroll][VEC];
-#pragma unroll
-            for (int i = 0; i < kAppUnroll; ++i) {
-                const int x = x0 + i * HG;
-                if (x < rows) {
-                    const T *src = x < q_rows       ? reinterpret_cast<const T *>(p.q) + b * p.qs[0] + x * p.qs[1] + t * p.qs[2]
-                                   : x < q_rows + H ? reinterpret_cast<const T *>(p.k) + b * p.ks[0] + (x - q_rows) * p.ks[1] + t * p.ks[2]
-                                                    : reinterpret_cast<const T *>(p.v) + b * p.vs[0] + (x - q_rows - H) * p.vs[1] + t * p.vs[2];
-                    Row<T, VEC>::load(src + rc.a, u[i]);
-                    if (rc.b >= 0) Row<T, VEC>::load(src + rc.b, w[i]);
-                }
-            }
+        for (int x0 = hg;;) {
 #pragma unroll
             for (int i = 0; i < kAppUnroll; ++i) {
                 const int x = x0 + i * HG;
@@ -87,12 +90,10 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
                     T *dst;
                     if (x < q_rows) {
                         dst = reinterpret_cast<T *>(p.q_out) + (((int64_t)b * p.Hq + x) * p.T + t) * d;
-                        rc.turn(u[i], w[i]);
                     } else if (x < q_rows + H) {
                         const int h = x - q_rows;
                         const int64_t row = pool_row(p.c, pg, h, in_page);
                         dst = reinterpret_cast<T *>(p.c.k) + row * d;
-                        rc.turn(u[i], w[i]);
                         if (chunk == 0) {
                             if (p.c.mass) p.c.mass[row] = p.mass_in ? p.mass_in[((int64_t)b * H + h) * p.T + t] : 0.f;
                             if (p.c.pos) p.c.pos[row] = (int32_t)position;
@@ -100,10 +101,12 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
                     } else {
                         dst = reinterpret_cast<T *>(p.c.v) + pool_row(p.c, pg, x - q_rows - H, in_page) * d;
                     }
-                    Row<T, VEC>::store(dst + rc.a, u[i]);
-                    if (rc.b >= 0) Row<T, VEC>::store(dst + rc.b, w[i]);
+                    rc.store(dst, u[i], w[i], x < q_rows + H);
                 }
             }
+            x0 += kAppUnroll * HG;
+            if (x0 >= rows) break;
+            load(x0);
         }
     }
     if (advance) {  // this block is the row's only one
@@ -116,6 +119,7 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
 }
 
 __global__ void append_advance_kernel(const __grid_constant__ AppendParams p) {
+    sm100::griddep_wait();
     int64_t len, clock;
     bool bad;
     const int64_t n = append_count(p, blockIdx.x, len, clock, bad);
@@ -135,8 +139,22 @@ cudaError_t launch_append_vec(const AppendParams &p, cudaStream_t s) {
     if ((int64_t)p.c.B * tiles > 0x7fffffffll) return cudaErrorInvalidValue;
     // a row that one block covers advances its own clock; else a second kernel
     // does, after every block has read it
-    append_kernel<T, VEC><<<(unsigned)(p.c.B * tiles), kAppThreads, 0, s>>>(p, chunks, tokens, (int)tiles, tiles == 1);
-    if (tiles > 1) append_advance_kernel<<<p.c.B, 128, 0, s>>>(p);
+    const unsigned grid = (unsigned)(p.c.B * tiles);
+    if (p.table.interleaved) append_kernel<T, VEC, true><<<grid, kAppThreads, 0, s>>>(p, chunks, tokens, (int)tiles, tiles == 1);
+    else append_kernel<T, VEC, false><<<grid, kAppThreads, 0, s>>>(p, chunks, tokens, (int)tiles, tiles == 1);
+    if (tiles > 1) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)p.c.B);
+        cfg.blockDim = dim3(128);
+        cfg.stream = s;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, append_advance_kernel, p);
+        if (e != cudaSuccess) return e;
+    }
     return cudaGetLastError();
 }
 
@@ -161,16 +179,17 @@ __device__ __forceinline__ void cluster_sync() {
 // ---- at most one pair leaves (the steady state; the step's first kernel) ----------
 //
 // The slice of A comes in by one bulk copy while the weights are looked
-// through, so it holds no registers; with d^2 / slices floats a block (32 KB at
-// most) several blocks share an SM and cover one another's latencies, of which
-// the chain length -> table -> weights -> pair -> A has many.
-constexpr int kOneThreads = 256;
-constexpr int kOneWarps = kOneThreads / 32;
+// through, so it holds no registers and two or more blocks share an SM and cover
+// one another's latencies, of which the chain length -> table -> weights -> pair
+// -> A has many.  (Blocks of half of A, each looking through the weights on its
+// own, spent more instructions on that than they saved: 30 us.)
+constexpr int one_threads(int d) { return d == 128 ? 512 : 256; }
 constexpr int kQBatch = 4;    // query heads per pass over A
-constexpr int kScanBatch = 8; // weights in flight per thread
+constexpr int kScanBatch = 4; // weights in flight per thread
 
 template <typename T, int D, bool STEP>
-__global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_constant__ EvictParams p, int slices) {
+__global__ void __launch_bounds__(one_threads(D), 1024 / one_threads(D)) evict_one_kernel(const __grid_constant__ EvictParams p, int slices) {
+    constexpr int kOneThreads = one_threads(D), kOneWarps = kOneThreads / 32;
     constexpr int CG = D / 4;              // float4 columns of A
     constexpr int RG = kOneThreads / CG;   // rows of A side by side
     extern __shared__ __align__(128) unsigned char dyn[];
@@ -241,9 +260,9 @@ __global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_
     }
     const int n = (int)n64, keep = n - m;
     const int32_t *table = c.table + (int64_t)b * c.max_pages;
-    auto row_of = [&](int slot) {
+    auto row_of = [&](int slot) {  // below 2^31
         const int pg = c.page_of(slot);
-        return pool_row(c, table[pg], h, slot - pg * c.page);
+        return (table[pg] * c.H + h) * c.page + slot - pg * c.page;
     };
     T *kp = reinterpret_cast<T *>(c.k), *vp = reinterpret_cast<T *>(c.v);
 
@@ -256,7 +275,7 @@ __global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_
         for (int i = 0; i < kScanBatch; ++i) {
             const int s = s0 + i * kOneThreads;
             if (s < seen) {
-                const int64_t row = row_of(s);
+                const int row = row_of(s);
                 w[i] = c.mass[row];
                 z[i] = c.pos[row];
             }
@@ -272,7 +291,7 @@ __global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_
         auto turned = [&](float f, float g, int i) {  // element i, its pair's other element g
             const int pair = rt.interleaved ? i / 2 : i < half ? i : i - half;
             const bool second = rt.interleaved ? (i & 1) : i >= half;
-            return second ? g * s_sin[pair] + f * s_cos[pair] : f * s_cos[pair] - g * s_sin[pair];
+            return rotated(f, g, s_cos[pair], second ? s_sin[pair] : -s_sin[pair]);
         };
         auto other = [&](int i) { return rt.interleaved ? i ^ 1 : i < half ? i + half : i - half; };
         const int64_t row = row_of(n - 1);
@@ -317,7 +336,7 @@ __global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_
                 const int s = s0 + i * kOneThreads;
                 if (s < seen) {
                     const uint64_t key = leave_key(w[i], z[i], protect_from);
-                    if (less_pair(key, (uint32_t)s, best, slot)) {
+                    if (key < best) {  // equal pairs: the earlier slot, seen first
                         best = key;
                         slot = (uint32_t)s;
                     }
@@ -391,7 +410,7 @@ __global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_
                         const int pair = p.table.interleaved ? i / 2 : i < half ? i : i - half;
                         const bool second = p.table.interleaved ? (i & 1) : i >= half;
                         const float y = to_f32(src[p.table.interleaved ? i ^ 1 : i < half ? i + half : i - half]);
-                        f = second ? y * s_sin[pair] + f * s_cos[pair] : f * s_cos[pair] - y * s_sin[pair];
+                        f = rotated(f, y, s_cos[pair], second ? s_sin[pair] : -s_sin[pair]);
                     }
                     s_q[g][i] = to_f32(from_f32<T>(f));
                 }
@@ -1064,7 +1083,7 @@ cudaError_t launch_one(const EvictParams &p, int slices, cudaStream_t s) {
     cudaError_t e = allow_smem(evict_one_kernel<T, D, STEP>, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = cluster_launch(attr, (int64_t)p.c.B * p.c.H * slices, kOneThreads, smem, slices, false, s);
+    const cudaLaunchConfig_t cfg = cluster_launch(attr, (int64_t)p.c.B * p.c.H * slices, one_threads(D), smem, slices, false, s);
     return cudaLaunchKernelEx(&cfg, evict_one_kernel<T, D, STEP>, p, slices);
 }
 
@@ -1111,9 +1130,9 @@ cudaError_t launch_one_d(const EvictParams &p, int d, int slices, cudaStream_t s
 }
 
 // Slices a head's A is cut into, one block of a cluster each, of 16 rows at
-// least: more while the device has room for them, `least` at any rate.
-int slices_for(int64_t BH, int d, int least, int most, int num_sms) {
-    int slices = least;
+// least: more while the device has room for them.
+int slices_for(int64_t BH, int d, int most, int num_sms) {
+    int slices = 1;
     while (slices * 2 <= d / 16 && slices < most && BH * slices * 2 <= 2 * num_sms) slices *= 2;
     return slices;
 }
@@ -1132,8 +1151,7 @@ cudaError_t launch_cache_append(const AppendParams &p, tc_dtype dtype, cudaStrea
     return wide ? launch_append_vec<float, 4>(p, s) : launch_append_vec<float, 1>(p, s);
 }
 
-// 32 KB of A a block at most, so that several share an SM.
-int evict_slices(int64_t BH, int d, int num_sms) { return slices_for(BH, d, d == 128 ? 2 : 1, 4, num_sms); }
+int evict_slices(int64_t BH, int d, int num_sms) { return slices_for(BH, d, 4, num_sms); }
 
 namespace {
 // Blocks that share a head's pairs: 1, 2 or 4 (2 for the narrow heads, whose sums
