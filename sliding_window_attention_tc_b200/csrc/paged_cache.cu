@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kAppThreads, 4) append_kernel(const __grid_con
         }
     };
     load(hg);
+    sm100::griddep_launch_dependents();  // the clocks' kernel waits for this one's end by itself
     int64_t len, clock;
     bool bad;
     const int64_t n = append_count(p, b, len, clock, bad);
@@ -178,21 +179,21 @@ __device__ __forceinline__ void cluster_sync() {
 
 // ---- at most one pair leaves (the steady state; the step's first kernel) ----------
 //
-// The slice of A comes in by one bulk copy while the weights are looked
-// through, so it holds no registers and two or more blocks share an SM and cover
-// one another's latencies, of which the chain length -> table -> weights -> pair
-// -> A has many.  (Blocks of half of A, each looking through the weights on its
-// own, spent more instructions on that than they saved: 30 us.)
-constexpr int one_threads(int d) { return d == 128 ? 512 : 256; }
+// What it waits for is the chain length -> table -> weights -> pair -> A: A is
+// asked into L2 at the start, and the blocks are small enough (64 registers, 20
+// KB) that four share an SM: 512 (row, head) of a serving step run at once.
+// (With A staged in shared memory two shared an SM, in two waves: 26 us; half of
+// A a block, twice the blocks: 30 us.)
+constexpr int kOneThreads = 256;
+constexpr int kOneWarps = kOneThreads / 32;
 constexpr int kQBatch = 4;    // query heads per pass over A
 constexpr int kScanBatch = 4; // weights in flight per thread
 
 template <typename T, int D, bool STEP>
-__global__ void __launch_bounds__(one_threads(D), 1024 / one_threads(D)) evict_one_kernel(const __grid_constant__ EvictParams p, int slices) {
-    constexpr int kOneThreads = one_threads(D), kOneWarps = kOneThreads / 32;
+__global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_constant__ EvictParams p, int slices) {
     constexpr int CG = D / 4;              // float4 columns of A
     constexpr int RG = kOneThreads / CG;   // rows of A side by side
-    extern __shared__ __align__(128) unsigned char dyn[];
+    constexpr int AU = 4;                  // float4 of A in flight per thread
     __shared__ __align__(16) float s_k[D], s_v[D];            // the pair that leaves
     __shared__ __align__(16) T s_new[2][D];                   // the new pair
     __shared__ float s_cos[D / 2 + 1], s_sin[D / 2 + 1];
@@ -200,21 +201,19 @@ __global__ void __launch_bounds__(one_threads(D), 1024 / one_threads(D)) evict_o
     __shared__ uint32_t s_slot[kOneWarps];
     __shared__ float s_q[kQBatch][D];
     __shared__ __align__(16) float s_mp[RG][kQBatch][D];
-    __shared__ __align__(8) uint64_t s_bar;
-    __shared__ int s_abort;
 
     const CacheParams &c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x % slices;
     const int64_t bh = blockIdx.x / slices;
     const int b = (int)(bh / c.H), h = (int)(bh % c.H);
+    sm100::griddep_launch_dependents();  // the next kernel waits for this one's end by itself
     const int64_t held = c.len[b], clock0 = c.clock[b];
     const int G = STEP ? p.Hq / c.H : 0;
     const bool first = h == 0 && rank == 0 && tid == 0;
     const int rows = D / slices, row0 = rank * rows;
     const bool read = STEP && p.memo != nullptr;
     float4 *A4 = c.A ? reinterpret_cast<float4 *>(c.A + (bh * D + row0) * D) : nullptr;
-    float4 *sA = reinterpret_cast<float4 *>(dyn);
 
     // the new token's rows do not wait for the length
     constexpr int NEW = (2 * D + kOneThreads - 1) / kOneThreads;
@@ -235,29 +234,15 @@ __global__ void __launch_bounds__(one_threads(D), 1024 / one_threads(D)) evict_o
     const int64_t over = n64 - p.budget;
     const int m = over <= 0 ? 0 : STEP ? 1 : over == 1 ? 1 : 0;
     bool ok = held >= 0 && n64 <= c.capacity() && held <= c.capacity() && (!STEP || (clock0 >= 0 && clock0 < (int64_t(1) << 31)));
-    const bool copy = A4 && ok && (read || m == 1);
-    if (tid == 0) {
-        s_abort = 0;
-        sm100::mbar_init(&s_bar, 1);
-        sm100::fence_mbar_init();
-        if (copy) {
-            sm100::mbar_expect_tx(&s_bar, (uint32_t)(rows * D * 4));
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             sm100::smem_u32(dyn)),
-                         "l"(A4), "r"(rows * D * 4), "r"(sm100::smem_u32(&s_bar))
-                         : "memory");
-        }
-    }
-    const bool in_range = ok;
-    if (ok) ok = block_pages_ok(c, b, 0, n64 - 1);  // its barrier also publishes s_bar, s_cos, s_sin
+    const bool use_A = A4 && ok && (read || m == 1);
+    if (use_A && tid == 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(A4), "r"(rows * D * 4) : "memory");
+    if (ok) ok = block_pages_ok(c, b, 0, n64 - 1);  // its barrier also publishes s_cos, s_sin
     if (first) {
         if (held >= 0 && !ok) report(c.status, TC_ERR_DEVICE_BOUNDS);
         p.row_len[b] = !ok ? -1 : STEP ? n64 - m : n64;
     }
-    if (!ok || (m == 0 && !STEP)) {
-        if (copy && in_range && tid == 0) sm100::mbar_wait_drain(&s_bar, 0);
-        return;  // the whole cluster
-    }
+    if (!ok || (m == 0 && !STEP)) return;  // the whole cluster
     const int n = (int)n64, keep = n - m;
     const int32_t *table = c.table + (int64_t)b * c.max_pages;
     auto row_of = [&](int slot) {  // below 2^31
@@ -376,7 +361,7 @@ __global__ void __launch_bounds__(one_threads(D), 1024 / one_threads(D)) evict_o
         gone = (int)slot;
     }
 
-    if (copy) {
+    if (use_A) {
         if (m == 1) {
             const bool is_new = STEP && gone == n - 1;
             const int64_t row = is_new ? 0 : row_of(gone);
@@ -388,13 +373,12 @@ __global__ void __launch_bounds__(one_threads(D), 1024 / one_threads(D)) evict_o
                 else s_k[e] = to_f32(x);
             }
         }
-        if (!sm100::mbar_wait(&s_bar, 0, &s_abort, c.status, p.wait_ns)) sm100::mbar_wait_drain(&s_bar, 0);
         __syncthreads();
     }
     // every block of the cluster that gets here has read the pair that leaves:
     // the barrier is waited for where its slot is written
     if (m == 1 && slices > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    if (copy) {
+    if (use_A) {
         const int cg = tid % CG, rg = tid / CG;
         const float lam = c.lam[h], eta = c.eta[h];
         const float4 v4 = m == 1 ? reinterpret_cast<const float4 *>(s_v)[cg] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -419,26 +403,32 @@ __global__ void __launch_bounds__(one_threads(D), 1024 / one_threads(D)) evict_o
             float4 mp[kQBatch];
 #pragma unroll
             for (int g = 0; g < kQBatch; ++g) mp[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int r = rg; r < rows; r += RG) {
-                float4 a = sA[r * CG + cg];
-                if (g0 == 0 && m == 1) {
-                    const float ek = eta * s_k[row0 + r];
-                    a.x = fmaf(lam, a.x, ek * v4.x);
-                    a.y = fmaf(lam, a.y, ek * v4.y);
-                    a.z = fmaf(lam, a.z, ek * v4.z);
-                    a.w = fmaf(lam, a.w, ek * v4.w);
-                    A4[r * CG + cg] = a;
-                    if (G > kQBatch) sA[r * CG + cg] = a;
-                }
-                if (read) {
+            for (int r0 = rg; r0 < rows; r0 += AU * RG) {
+                float4 a[AU];
 #pragma unroll
-                    for (int g = 0; g < kQBatch; ++g) {
-                        const float x = s_q[g][row0 + r];  // heads past the last: never stored
-                        mp[g].x = fmaf(x, a.x, mp[g].x);
-                        mp[g].y = fmaf(x, a.y, mp[g].y);
-                        mp[g].z = fmaf(x, a.z, mp[g].z);
-                        mp[g].w = fmaf(x, a.w, mp[g].w);
+                for (int i = 0; i < AU; ++i)
+                    if (r0 + i * RG < rows) a[i] = A4[(r0 + i * RG) * CG + cg];
+#pragma unroll
+                for (int i = 0; i < AU; ++i) {
+                    const int r = r0 + i * RG;
+                    if (r >= rows) break;
+                    if (g0 == 0 && m == 1) {
+                        const float ek = eta * s_k[row0 + r];
+                        a[i].x = fmaf(lam, a[i].x, ek * v4.x);
+                        a[i].y = fmaf(lam, a[i].y, ek * v4.y);
+                        a[i].z = fmaf(lam, a[i].z, ek * v4.z);
+                        a[i].w = fmaf(lam, a[i].w, ek * v4.w);
+                        A4[r * CG + cg] = a[i];  // (later batches read it back)
+                    }
+                    if (read) {
+#pragma unroll
+                        for (int g = 0; g < kQBatch; ++g) {
+                            const float x = s_q[g][row0 + r];  // heads past the last: never stored
+                            mp[g].x = fmaf(x, a[i].x, mp[g].x);
+                            mp[g].y = fmaf(x, a[i].y, mp[g].y);
+                            mp[g].z = fmaf(x, a[i].z, mp[g].z);
+                            mp[g].w = fmaf(x, a[i].w, mp[g].w);
+                        }
                     }
                 }
             }
@@ -1079,11 +1069,8 @@ cudaLaunchConfig_t cluster_launch(cudaLaunchAttribute *attr, int64_t grid, int t
 
 template <typename T, int D, bool STEP>
 cudaError_t launch_one(const EvictParams &p, int slices, cudaStream_t s) {
-    const size_t smem = p.c.A ? (size_t)D * D / slices * sizeof(float) : 0;
-    cudaError_t e = allow_smem(evict_one_kernel<T, D, STEP>, smem);
-    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = cluster_launch(attr, (int64_t)p.c.B * p.c.H * slices, one_threads(D), smem, slices, false, s);
+    const cudaLaunchConfig_t cfg = cluster_launch(attr, (int64_t)p.c.B * p.c.H * slices, kOneThreads, 0, slices, false, s);
     return cudaLaunchKernelEx(&cfg, evict_one_kernel<T, D, STEP>, p, slices);
 }
 
