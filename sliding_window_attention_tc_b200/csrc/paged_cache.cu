@@ -482,6 +482,7 @@ __global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_
 constexpr int kBulkThreads = 512;
 constexpr int kBulkWarps = kBulkThreads / 32;
 constexpr int kSortMax = 8192;   // pairs sorted in shared memory (16 bytes each)
+constexpr int kPickMax = 32;     // pairs picked one after the other instead (rows of up to 32 * 512)
 
 // lambda^j for j >= 0 to float32's precision: the exponent in 64 bits, its
 // fraction to exp2f.
@@ -732,6 +733,8 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ int s_scan[kBulkWarps];
     __shared__ uint32_t s_total[32], s_base[kBulkWarps][32], s_bits[4][kBulkWarps];
+    __shared__ uint64_t s_pick[2][kBulkWarps];
+    __shared__ uint32_t s_pick_slot[2][kBulkWarps];
 
     const CacheParams &c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -820,8 +823,52 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
 #pragma unroll
             for (int i = 0; i < 4; ++i) differ[i] |= s_bits[i][w];
         const uint32_t w_differ = differ[0] & differ[1], z_differ = differ[2] & differ[3];
-        const uint32_t *from;
-        if (inside) {
+        const uint32_t *from = order;
+        if (m <= kPickMax && n <= 32 * kBulkThreads) {
+            // few leave: the first of what is left, m times; each thread knows the
+            // first of its own slots
+            uint32_t gone = 0, slot;
+            uint64_t first;
+            auto look = [&]() {
+                first = ~0ull;
+                slot = 0xffffffffu;
+                for (int s = tid, j = 0; s < n; s += kBulkThreads, ++j) {
+                    const uint64_t key = (uint64_t)(place[s] >> 31) << 63 | (uint64_t)weight[s] << 31 | (place[s] & 0x7fffffffu);
+                    if (!(gone >> (j & 31) & 1u) && key < first) {
+                        first = key;
+                        slot = (uint32_t)s;
+                    }
+                }
+            };
+            // the least (key, slot) of the lanes
+            auto least = [&](uint64_t &k, uint32_t &s) {
+                const uint32_t hi = __reduce_min_sync(0xffffffffu, (uint32_t)(k >> 32));
+                const uint32_t lo = __reduce_min_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0xffffffffu);
+                s = __reduce_min_sync(0xffffffffu, (uint32_t)(k >> 32) == hi && (uint32_t)k == lo ? s : 0xffffffffu);
+                k = (uint64_t)hi << 32 | lo;
+            };
+            look();
+            for (int i = 0; i < m; ++i) {
+                uint64_t k = first;
+                uint32_t s = slot;
+                least(k, s);
+                if (lane == 0) {
+                    s_pick[i & 1][warp] = k;
+                    s_pick_slot[i & 1][warp] = s;
+                }
+                __syncthreads();
+                k = lane < kBulkWarps ? s_pick[i & 1][lane] : ~0ull;
+                s = lane < kBulkWarps ? s_pick_slot[i & 1][lane] : 0xffffffffu;
+                least(k, s);
+                if ((int)(s % kBulkThreads) == tid) {
+                    other[i] = s;
+                    gone |= 1u << (s / kBulkThreads);
+                    look();
+                }
+            }
+            __syncthreads();
+            from = other;
+        } else if (inside) {
             // the same addresses, from the block's own shared memory, so that they
             // are accessed as such
             uint32_t *o = reinterpret_cast<uint32_t *>(dyn), *w = reinterpret_cast<uint32_t *>(dyn + order_room(n_cap));

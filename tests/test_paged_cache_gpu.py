@@ -252,6 +252,20 @@ def test_evict(cuda_device, dtype, d, H, held, budget, recent):
     same_state(c, cpu, A_terms=max(held))
 
 
+@pytest.mark.parametrize("m", [2, 3, 31, 32, 33, 64])
+def test_evict_few_and_more(cuda_device, m):
+    """Numbers around the one up to which pairs are picked one after the other, in
+    rows longer than a block has threads, many heads to a cluster."""
+    import sliding_window_attention_tc_b200 as tc
+    held = [600 + m, 600, 1300, 600 + m] + [40 + m] * 40
+    c, cpu = make(held, d=16, H=9, dtype="f32", seed=m, room=0)
+    for budget in (600, 40):
+        tc.cache_evict(c, budget, recent=16)
+        cpu.evict(budget, 16)
+        same_state(c, cpu, A_terms=1300)
+    assert tc.device_status() == 0
+
+
 def test_evict_odd_weights(cuda_device):
     """Zeros of both signs, infinities, NaN, negative weights, equal positions,
     a recent window wider than the budget; no memory; decays 0, 1 and negative."""
