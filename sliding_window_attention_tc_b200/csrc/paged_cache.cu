@@ -468,9 +468,10 @@ __global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_
 // ---- several pairs leave ------------------------------------------------------------
 //
 // The slots are sorted by (protected, mass, pos) with a stable radix sort, in
-// shared memory up to kSortMax pairs, over the bits in which pairs differ.  (2559
-// pairs: a bitonic sort of the keys took 139,000 cycles, 8 bits a pass with a
-// warp's lanes matched against one another 82,000, 4 bits as below 41,000.)  The
+// shared memory up to kSortMax pairs, over the bits in which pairs differ; or,
+// where the weights spread, by counting them into buckets first.  (2559 pairs: a
+// bitonic sort of the keys took 139,000 cycles, a radix sort of 8 bits a pass with a
+// warp's lanes matched against one another 82,000, the one below 41,000.)  The
 // weighted sum runs on the tensor cores: tiles of TP pairs come in by
 // asynchronous 16-byte copies, several in flight; the weighted keys
 // lambda^(m-1-i) k_i are split into three bf16 parts (24 bits together; a
@@ -659,6 +660,73 @@ __device__ __forceinline__ uint32_t *sort_slots(uint32_t *order, uint32_t *other
     return swapped ? other : order;
 }
 
+// The same order, for weights that spread: the slots are counted into buckets
+// by weight (the bits of a float are its logarithm, so even steps of the bits
+// spread weights of any scale; zeros, of which there may be many, have a bucket of
+// their own; protected pairs theirs behind the others), and each finds its place
+// among its bucket's few by comparing.  False, and nothing done, when that would
+// be more than kCompareMost comparisons a slot.  lo, hi: the least weight above zero and the
+// greatest, as ordered bits; none below zero.
+constexpr int kBuckets = 4096;     // plain and protected; 16-bit counters, two to a word
+constexpr int kCompareMost = 64;
+
+__device__ bool bucket_sort(uint32_t *order, uint32_t *other, const uint32_t *weight, const uint32_t *place, int n, uint32_t lo, uint32_t hi,
+                            uint32_t *words, int *scan) {
+    const int tid = threadIdx.x;
+    const int shift = max(0, 32 - __clz(hi - lo) - 11);  // (hi - lo) >> shift below 2048
+    auto bucket = [&](uint32_t s) {
+        const uint32_t v = weight[s];
+        return (place[s] >> 31) * (kBuckets / 2) + (v == 0x80000000u ? 0u : min(1u + ((v - lo) >> shift), (uint32_t)kBuckets / 2 - 1));
+    };
+    for (int x = tid; x < kBuckets / 2; x += kBulkThreads) words[x] = 0;
+    __syncthreads();
+    for (int s = tid; s < n; s += kBulkThreads) {
+        const uint32_t b = bucket(s);
+        atomicAdd(words + b / 2, 1u << (b % 2 * 16));
+    }
+    __syncthreads();
+    constexpr int PER = kBuckets / 2 / kBulkThreads;  // words of a thread
+    static_assert(PER == 4, "one vector");
+    uint4 w = reinterpret_cast<const uint4 *>(words)[tid];
+    uint32_t c[2 * PER] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16, w.z & 0xffffu, w.z >> 16, w.w & 0xffffu, w.w >> 16};
+    int sum = 0, compared = 0, total;
+#pragma unroll
+    for (int i = 0; i < 2 * PER; ++i) {
+        compared += (int)(c[i] * c[i]);  // below 2^27 in all
+        sum += (int)c[i];
+    }
+    block_scan(compared, scan, &total);
+    if (total > kCompareMost * n) return false;
+    uint32_t at = (uint32_t)block_scan(sum, scan, &total);
+#pragma unroll
+    for (int i = 0; i < 2 * PER; ++i) {
+        const uint32_t x = c[i];
+        c[i] = at;
+        at += x;
+    }
+    reinterpret_cast<uint4 *>(words)[tid] = make_uint4(c[0] | c[1] << 16, c[2] | c[3] << 16, c[4] | c[5] << 16, c[6] | c[7] << 16);
+    __syncthreads();
+    for (int s = tid; s < n; s += kBulkThreads) {
+        const uint32_t b = bucket(s);
+        other[(atomicAdd(words + b / 2, 1u << (b % 2 * 16)) >> (b % 2 * 16)) & 0xffffu] = s;
+    }
+    __syncthreads();
+    // the counters are the buckets' ends now
+    for (int i = tid; i < n; i += kBulkThreads) {
+        const uint32_t s = other[i], b = bucket(s), v = weight[s], z = place[s];
+        const uint32_t begin = b ? words[(b - 1) / 2] >> ((b - 1) % 2 * 16) & 0xffffu : 0u, end = words[b / 2] >> (b % 2 * 16) & 0xffffu;
+        uint32_t to = begin;
+#pragma unroll 4
+        for (uint32_t j = begin; j < end; ++j) {
+            const uint32_t x = other[j], vx = weight[x], zx = place[x];  // (within a bucket z's top bits agree)
+            to += vx < v || (vx == v && (zx < z || (zx == z && x < s)));
+        }
+        order[to] = s;
+    }
+    __syncthreads();
+    return true;
+}
+
 __device__ __forceinline__ void ldsm_t4(const void *p, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -732,8 +800,9 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
     using S = BulkShape<T, D>;
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ int s_scan[kBulkWarps];
-    __shared__ uint32_t s_total[32], s_base[kBulkWarps][32], s_bits[4][kBulkWarps];
+    __shared__ uint32_t s_total[32], s_base[kBulkWarps][32], s_bits[7][kBulkWarps];
     __shared__ uint64_t s_pick[2][kBulkWarps];
+    __shared__ float s_pow[64 + kSortMax / 64];
     __shared__ uint32_t s_pick_slot[2][kBulkWarps];
 
     const CacheParams &c = p.c;
@@ -769,6 +838,7 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
         const int64_t protect_from = c.clock[b] - p.recent;
         bool sorted = true;  // by position already, as tokens are appended
         uint32_t w_or = 0, w_and = ~0u, z_or = 0, z_and = ~0u;  // bits that differ between pairs
+        uint32_t w_lo = ~0u, w_hi = 0, w_min = ~0u;             // least above zero, greatest, least
         constexpr int U = 8;
         for (int s0 = tid; s0 < n; s0 += U * kBulkThreads) {
             float w[U];
@@ -795,6 +865,9 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
                     w_and &= weight[s];
                     z_or |= place[s];
                     z_and &= place[s];
+                    w_min = min(w_min, weight[s]);
+                    w_hi = max(w_hi, weight[s]);
+                    if (weight[s] != 0x80000000u) w_lo = min(w_lo, weight[s]);
                 }
             }
         }
@@ -803,18 +876,21 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
         for (int s = tid; s + 1 < n; s += kBulkThreads)
             sorted = sorted && (place[s] & 0x7fffffffu) <= (place[s + 1] & 0x7fffffffu);
         const bool by_place = !__syncthreads_and(sorted);
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) {
-            w_or |= __shfl_xor_sync(0xffffffffu, w_or, o);
-            w_and &= __shfl_xor_sync(0xffffffffu, w_and, o);
-            z_or |= __shfl_xor_sync(0xffffffffu, z_or, o);
-            z_and &= __shfl_xor_sync(0xffffffffu, z_and, o);
-        }
+        w_or = __reduce_or_sync(0xffffffffu, w_or);
+        w_and = __reduce_and_sync(0xffffffffu, w_and);
+        z_or = __reduce_or_sync(0xffffffffu, z_or);
+        z_and = __reduce_and_sync(0xffffffffu, z_and);
+        w_lo = __reduce_min_sync(0xffffffffu, w_lo);
+        w_min = __reduce_min_sync(0xffffffffu, w_min);
+        w_hi = __reduce_max_sync(0xffffffffu, w_hi);
         if (lane == 0) {
             s_bits[0][warp] = w_or;
             s_bits[1][warp] = ~w_and;
             s_bits[2][warp] = z_or;
             s_bits[3][warp] = ~z_and;
+            s_bits[4][warp] = ~w_lo;
+            s_bits[5][warp] = ~w_min;
+            s_bits[6][warp] = w_hi;
         }
         __syncthreads();
         uint32_t differ[4] = {0, 0, 0, 0};
@@ -822,6 +898,10 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
         for (int w = 0; w < kBulkWarps; ++w)
 #pragma unroll
             for (int i = 0; i < 4; ++i) differ[i] |= s_bits[i][w];
+        const uint32_t mine = lane < kBulkWarps ? s_bits[4][lane] : 0u, low = lane < kBulkWarps ? s_bits[5][lane] : 0u;
+        w_lo = ~__reduce_max_sync(0xffffffffu, mine);
+        w_min = ~__reduce_max_sync(0xffffffffu, low);
+        w_hi = __reduce_max_sync(0xffffffffu, lane < kBulkWarps ? s_bits[6][lane] : 0u);
         const uint32_t w_differ = differ[0] & differ[1], z_differ = differ[2] & differ[3];
         const uint32_t *from = order;
         if (m <= kPickMax && n <= 32 * kBulkThreads) {
@@ -872,10 +952,12 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
             // the same addresses, from the block's own shared memory, so that they
             // are accessed as such
             uint32_t *o = reinterpret_cast<uint32_t *>(dyn), *w = reinterpret_cast<uint32_t *>(dyn + order_room(n_cap));
+            const bool spread = w_min >= 0x80000000u && w_lo < w_hi;  // no weight below zero, two above
             auto sort = [&](auto items) {
                 return sort_slots<decltype(items)::value>(o, w + 2 * n_cap, w, w + n_cap, n, by_place, w_differ, z_differ, w + 3 * n_cap, s_total, s_base);
             };
-            from = n <= kBulkThreads       ? sort(std::integral_constant<int, 1>())
+            from = spread && bucket_sort(o, w + 2 * n_cap, w, w + n_cap, n, w_lo, w_hi, w + 3 * n_cap, s_scan) ? o
+                   : n <= kBulkThreads     ? sort(std::integral_constant<int, 1>())
                    : n <= 3 * kBulkThreads ? sort(std::integral_constant<int, 3>())
                    : n <= 5 * kBulkThreads ? sort(std::integral_constant<int, 5>())
                    : n <= 9 * kBulkThreads ? sort(std::integral_constant<int, 9>())
@@ -884,12 +966,17 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
             from = sort_slots<0>(order, other, weight, place, n, by_place, w_differ, z_differ, counts, s_total, s_base);
         }
         // the pairs that leave: marked, and from here on named by their pool rows
+        // (rows sorted in shared memory: lambda^(m-1-i) from its powers below 64 and of 64)
         const Decay decay(c.A ? c.lam[h] : 1.f);
+        if (inside)
+            for (int x = tid; x < 64 + kSortMax / 64; x += kBulkThreads) s_pow[x] = decay.pow(x < 64 ? x : (int64_t)(x - 64) * 64);
+        __syncthreads();
         for (int i = tid; i < m; i += kBulkThreads) {
             const uint32_t s = from[i];
+            const int e = m - 1 - i;
             atomicOr(&bits[s / 32], 1u << (s % 32));
+            factor[i] = inside ? s_pow[e & 63] * s_pow[64 + (e >> 6)] : decay.pow(e);
             order[i] = (uint32_t)row_of((int)s);
-            factor[i] = decay.pow(m - 1 - i);
         }
         __syncthreads();
     }
