@@ -473,13 +473,13 @@ __global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_
 // bitonic sort of the keys took 139,000 cycles, a radix sort of 8 bits a pass with a
 // warp's lanes matched against one another 82,000, the one below 41,000.)  The
 // weighted sum runs on the tensor cores: tiles of TP pairs come in by
-// asynchronous 16-byte copies, several in flight; the weighted keys
-// lambda^(m-1-i) k_i are split into three bf16 parts (24 bits together; a
-// float32 cache's values too), and the products' sums over one tile are added
-// to float32 sums with the ordinary rounding, because the tensor cores' own
-// accumulation truncates and would drift over thousands of pairs.  The blocks
-// of a cluster take every SL-th tile and add their sums through one another's
-// shared memory.
+// asynchronous 16-byte copies, several in flight; a warp takes 16 pairs and 16 of
+// A's rows, makes the weighted keys lambda^(m-1-i) k_i in registers, in three bf16
+// parts (24 bits together; a float32 cache's values too), and the products' sums
+// over one tile are added to float32 sums with the ordinary rounding, because the
+// tensor cores' own accumulation truncates and would drift over thousands of
+// pairs.  The blocks of a cluster take every SL-th tile and add their sums through
+// one another's shared memory.
 constexpr int kBulkThreads = 512;
 constexpr int kBulkWarps = kBulkThreads / 32;
 constexpr int kSortMax = 8192;   // pairs sorted in shared memory (16 bytes each)
@@ -733,12 +733,6 @@ __device__ __forceinline__ void ldsm_t4(const void *p, uint32_t (&r)[4]) {
                  : "r"(sm100::smem_u32(p))
                  : "memory");
 }
-__device__ __forceinline__ void ldsm_t2(const void *p, uint32_t (&r)[2]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
-                 : "=r"(r[0]), "=r"(r[1])
-                 : "r"(sm100::smem_u32(p))
-                 : "memory");
-}
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -772,20 +766,19 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t (&o)[3]) {
 // moves.
 template <typename T, int D>
 struct BulkShape {
-    static constexpr int TP = sizeof(T) == 2 ? 64 : 32;     // pairs per tile
-    static constexpr int STAGES = 3;
-    static constexpr int VPARTS = sizeof(T) == 2 ? 0 : 3;   // bf16 values go in as they are
-    static constexpr int KRAW = D * (int)sizeof(T);         // bytes of a raw row
-    static constexpr int VRAW = D * (int)sizeof(T) + 16;    // padded: conflict-free reads by ldmatrix
-    static constexpr int PS = D * 2 + 16;                   // bytes of a row of a part
-    static constexpr int RAW = TP * (KRAW + VRAW);
-    static constexpr int PARTS = TP * (3 + VPARTS) * PS;
-    static constexpr int SUM = STAGES * RAW + PARTS;        // at least the result's 4 D^2
-    // output tiles of 16 x 8: warps along the rows first
-    static constexpr int TM = D / 16, TN = D / 8, NWN = kBulkWarps / TM;
-    static constexpr int NT = TN / NWN > 0 ? TN / NWN : 1;  // tiles a warp holds
+    static constexpr bool F32 = sizeof(T) == 4;
+    static constexpr int TP = F32 ? 32 : 64;                // pairs per tile
+    static constexpr int STAGES = 4;
+    static constexpr int ROW = D * (int)sizeof(T) + 16;     // bytes of a row, padded: no bank conflicts
+    static constexpr int RAW = TP * 2 * ROW;                // keys, then values
+    static constexpr int SUM = STAGES * RAW;                // at least the result's 4 D^2
+    // A's tiles of 16 x 8: a warp takes one row of tiles (or half of one, at
+    // most 8), and one of KG parts of the pairs
+    static constexpr int TM = D / 16, TN = D / 8, NW = TN > 8 ? TN / 8 : 1, NT = TN / NW;
+    static constexpr int KS = TP / 16;                      // steps of 16 pairs in a tile
+    static constexpr int KG = kBulkWarps / (TM * NW) < KS ? kBulkWarps / (TM * NW) : KS;
     static_assert(kSortMax <= 17 * kBulkThreads, "sorted in registers");
-    static_assert(SUM >= 4 * D * D, "the block's sum has to fit");
+    static_assert(SUM >= 4 * D * D && KS % KG == 0, "the block's sum has to fit");
 };
 
 // Bytes of sorting room for up to n pairs (a multiple of 32): keys, positions,
@@ -983,9 +976,7 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
 
     // ---- A: lambda^m A + eta sum of lambda^(m-1-i) k_i v_i^T -------------------------
     if (c.A) {
-        unsigned char *parts = tiles_mem + S::STAGES * S::RAW;
-        const int wm = warp % S::TM, wn = (warp / S::TM) * S::NT;
-        const bool works = wn < S::TN;
+        const int wm = warp % S::TM, wn = warp / S::TM % S::NW * S::NT, kg = warp / (S::TM * S::NW);
         float sum[S::NT][4];
 #pragma unroll
         for (int t = 0; t < S::NT; ++t)
@@ -996,13 +987,13 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
             if (tile < tiles) {
                 unsigned char *raw = tiles_mem + (tile % S::STAGES) * S::RAW;
                 constexpr int RC = D * (int)sizeof(T) / 16, EL = 16 / (int)sizeof(T);  // chunks of a row, elements of one
-                for (int x = tid; x < S::TP * 2 * RC; x += kBulkThreads) {
-                    const int pr = x / (2 * RC), ch = x % (2 * RC);
+#pragma unroll
+                for (int x0 = 0; x0 < S::TP * 2 * RC; x0 += kBulkThreads) {
+                    const int x = x0 + tid, pr = x / (2 * RC), ch = x % (2 * RC);
+                    if (S::TP * 2 * RC % kBulkThreads != 0 && pr >= S::TP) break;
                     const int i = (tile * SL + rank) * S::TP + pr;
-                    const int64_t row = i < m ? (int64_t)order[i] : -1;
-                    unsigned char *dst = ch < RC ? raw + pr * S::KRAW + ch * 16 : raw + S::TP * S::KRAW + pr * S::VRAW + (ch - RC) * 16;
-                    const T *src = ch < RC ? kp + row * D + ch * EL : vp + row * D + (ch - RC) * EL;
-                    if (row >= 0) copy16(dst, src);
+                    unsigned char *dst = raw + ((ch < RC ? 0 : S::TP) + pr) * S::ROW + ch % RC * 16;
+                    if (i < m) copy16(dst, (ch < RC ? kp : vp) + (int64_t)order[i] * D + ch % RC * EL);
                     else zero16(dst);
                 }
             }
@@ -1011,51 +1002,74 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
         for (int i = 0; i < S::STAGES - 1; ++i) fetch(i);
         for (int tile = 0; tile < tiles; ++tile) {
             asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 2) : "memory");
-            __syncthreads();  // the tile is there; the parts and the last tile's buffer are free
+            __syncthreads();  // the tile is there; the last tile's buffer is free
             fetch(tile + S::STAGES - 1);
-            const unsigned char *raw = tiles_mem + (tile % S::STAGES) * S::RAW;
-            for (int x = tid; x < S::TP * D / 8; x += kBulkThreads) {  // eight elements a thread
-                const int pr = x / (D / 8), e = x % (D / 8), i = (tile * SL + rank) * S::TP + pr;
-                const float w = i < m ? factor[i] : 0.f;
-                auto part = [&](const unsigned char *src, float scale, int first) {
-                    float f[8];
-                    uint32_t o[4][3];
-#pragma unroll
-                    for (int y = 0; y < 8; y += Vec16<T>::N)
-                        Vec16<T>::unpack(reinterpret_cast<const uint4 *>(src + e * 8 * sizeof(T))[y / Vec16<T>::N], f + y);
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) split3(scale * f[2 * y], scale * f[2 * y + 1], o[y]);
-#pragma unroll
-                    for (int y = 0; y < 3; ++y)
-                        *reinterpret_cast<uint4 *>(parts + ((first + y) * S::TP + pr) * S::PS + e * 16) = make_uint4(o[0][y], o[1][y], o[2][y], o[3][y]);
-                };
-                part(raw + pr * S::KRAW, w, 0);
-                if (S::VPARTS) part(raw + S::TP * S::KRAW + pr * S::VRAW, 1.f, 3);
-            }
-            __syncthreads();
-            if (works) {
-                const unsigned char *vbase = S::VPARTS ? parts + 3 * S::TP * S::PS : raw + S::TP * S::KRAW;
-                constexpr int VROW = S::VPARTS ? S::PS : S::VRAW;
+            const unsigned char *keys = tiles_mem + (tile % S::STAGES) * S::RAW, *values = keys + S::TP * S::ROW;
+            if (kg < S::KG) {
                 float acc[S::NT][4];
 #pragma unroll
                 for (int t = 0; t < S::NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
 #pragma unroll
-                for (int k = 0; k < S::TP / 16; ++k) {
-                    // keys [pair][row]: as the transposed operand, pairs along k
+                for (int kk = 0; kk < S::KS / S::KG; ++kk) {
+                    const int k0 = (kg * (S::KS / S::KG) + kk) * 16, p0 = k0 + lane % 4 * 2;  // this lane's pairs: p0, +1, +8, +9
+                    float w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = (tile * SL + rank) * S::TP + p0 + (e & 1) + (e >> 1) * 8;
+                        w[e] = i < m ? factor[i] : 0.f;
+                    }
+                    // the weighted keys, transposed (rows of A by pairs), in three parts
                     uint32_t a[3][4];
+                    uint32_t raw[4];
+                    if (!S::F32) ldsm_t4(keys + (k0 + (lane & 7) + (lane >> 4) * 8) * S::ROW + (wm * 16 + ((lane >> 3) & 1) * 8) * 2, raw);
 #pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        ldsm_t4(parts + (i * S::TP + k * 16 + (lane & 7) + (lane >> 4) * 8) * S::PS + (wm * 16 + ((lane >> 3) & 1) * 8) * 2, a[i]);
+                    for (int r = 0; r < 4; ++r) {
+                        float x, y;  // row lane / 4 (+ 8), pairs p0, p0 + 1 (+ 8)
+                        if (S::F32) {
+                            const unsigned char *at = keys + (p0 + (r >> 1) * 8) * S::ROW + (wm * 16 + lane / 4 + (r & 1) * 8) * 4;
+                            x = *reinterpret_cast<const float *>(at);
+                            y = *reinterpret_cast<const float *>(at + S::ROW);
+                        } else {
+                            x = __uint_as_float(raw[r] << 16);
+                            y = __uint_as_float(raw[r] & 0xffff0000u);
+                        }
+                        uint32_t o[3];
+                        split3(w[(r >> 1) * 2] * x, w[(r >> 1) * 2 + 1] * y, o);
+                        a[0][r] = o[0];
+                        a[1][r] = o[1];
+                        a[2][r] = o[2];
+                    }
+                    if (S::F32) {
 #pragma unroll
-                    for (int t = 0; t < S::NT; ++t) {
+                        for (int t = 0; t < S::NT; ++t) {
+                            const unsigned char *at = values + p0 * S::ROW + ((wn + t) * 8 + lane / 4) * 4;
+                            uint32_t v[3][2];
 #pragma unroll
-                        for (int j = 0; j < (S::VPARTS ? 3 : 1); ++j) {
-                            uint32_t v[2];
-                            ldsm_t2(vbase + (j * S::TP + k * 16 + (lane & 15)) * VROW + (wn + t) * 16, v);
+                            for (int r = 0; r < 2; ++r) {
+                                uint32_t o[3];
+                                split3(*reinterpret_cast<const float *>(at + r * 8 * S::ROW), *reinterpret_cast<const float *>(at + (r * 8 + 1) * S::ROW), o);
+                                v[0][r] = o[0];
+                                v[1][r] = o[1];
+                                v[2][r] = o[2];
+                            }
 #pragma unroll
-                            for (int i = 2 - j; i >= 0; --i) mma_bf16(acc[t], a[i], v);
+                            for (int j = 2; j >= 0; --j)
+#pragma unroll
+                                for (int i = 2 - j; i >= 0; --i) mma_bf16(acc[t], a[i], v[j]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < S::NT; t += 2) {
+                            uint32_t v[4];  // two tiles' values
+                            ldsm_t4(values + (k0 + (lane & 7) + ((lane >> 3) & 1) * 8) * S::ROW + ((wn + t) * 8 + (lane >> 4) * 8) * 2, v);
+                            const uint32_t v0[2] = {v[0], v[1]}, v1[2] = {v[2], v[3]};
+#pragma unroll
+                            for (int i = 2; i >= 0; --i) {
+                                mma_bf16(acc[t], a[i], v0);
+                                mma_bf16(acc[t + 1], a[i], v1);
+                            }
                         }
                     }
                 }
@@ -1065,57 +1079,51 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
                     for (int e = 0; e < 4; ++e) sum[t][e] += acc[t][e];
             }
         }
-        const float lm = Decay(c.lam[h]).pow(m), eta = c.eta[h];
-        const int row = wm * 16 + lane / 4, col = (lane % 4) * 2;
-        if constexpr (SL == 1) {
-            if (works) {
+        // the parts of the pairs, added; then the blocks' sums
+        float *mine = reinterpret_cast<float *>(tiles_mem);  // [D][D]
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        for (int g = 0; g < S::KG; ++g) {
+            __syncthreads();
+            if (kg == g) {
 #pragma unroll
                 for (int t = 0; t < S::NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; e += 2) {
-                        float2 *x = reinterpret_cast<float2 *>(c.A + (bh * D + row + e * 4) * D + (wn + t) * 8 + col);
-                        float2 o = *x;
-                        o.x = fmaf(lm, o.x, eta * sum[t][e]);
-                        o.y = fmaf(lm, o.y, eta * sum[t][e + 1]);
-                        *x = o;
+                        float2 *x = reinterpret_cast<float2 *>(mine + (wm * 16 + lane / 4 + e * 4) * D + (wn + t) * 8 + lane % 4 * 2);
+                        const float2 o = g ? *x : make_float2(0.f, 0.f);
+                        *x = make_float2(o.x + sum[t][e], o.y + sum[t][e + 1]);
                     }
             }
-        } else {
-            float *mine = reinterpret_cast<float *>(tiles_mem);  // [D][D]
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            __syncthreads();
-            if (works) {
+        }
+        if (SL > 1) cluster_sync();
+        else __syncthreads();
+        const float lm = Decay(c.lam[h]).pow(m), eta = c.eta[h];
+        for (int at = rank * kBulkThreads + tid; at < D * D / 4; at += SL * kBulkThreads) {  // this block's share of A
+            float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int t = 0; t < S::NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2)
-                        *reinterpret_cast<float2 *>(mine + (row + e * 4) * D + (wn + t) * 8 + col) = make_float2(sum[t][e], sum[t][e + 1]);
-            }
-            cluster_sync();
-            // this block's share of A, from every block's sum
-            for (int at = rank * kBulkThreads + tid; at < D * D / 4; at += SL * kBulkThreads) {
-                float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int r = 0; r < SL; ++r) {
+            for (int r = 0; r < SL; ++r) {
+                float4 y;
+                if (SL > 1) {
                     uint32_t there;
-                    float4 y;
                     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(sm100::smem_u32(mine + at * 4)), "r"(r));
                     asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w) : "r"(there) : "memory");
-                    add.x += y.x;
-                    add.y += y.y;
-                    add.z += y.z;
-                    add.w += y.w;
+                } else {
+                    y = reinterpret_cast<const float4 *>(mine)[at];
                 }
-                float4 *dst = reinterpret_cast<float4 *>(c.A + bh * D * D) + at;
-                float4 o = *dst;
-                o.x = fmaf(lm, o.x, eta * add.x);
-                o.y = fmaf(lm, o.y, eta * add.y);
-                o.z = fmaf(lm, o.z, eta * add.z);
-                o.w = fmaf(lm, o.w, eta * add.w);
-                *dst = o;
+                add.x += y.x;
+                add.y += y.y;
+                add.z += y.z;
+                add.w += y.w;
             }
-            cluster_sync();  // the sums have been read: their room is free
+            float4 *dst = reinterpret_cast<float4 *>(c.A + bh * D * D) + at;
+            float4 o = *dst;
+            o.x = fmaf(lm, o.x, eta * add.x);
+            o.y = fmaf(lm, o.y, eta * add.y);
+            o.z = fmaf(lm, o.z, eta * add.z);
+            o.w = fmaf(lm, o.w, eta * add.w);
+            *dst = o;
         }
+        if (SL > 1) cluster_sync();  // the sums have been read: their room is free
     }
 
     // ---- freed slots below keep, and the pairs behind it that stay ------------------
