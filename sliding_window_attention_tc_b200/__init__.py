@@ -748,6 +748,9 @@ assert (_PACK_ROTATE.size, _PACK_APPEND.size, _PACK_STEP.size) == tuple(
     ctypes.sizeof(s) for s in (RotateDesc, AppendArgs, StepArgs))
 
 
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _addr(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -761,52 +764,58 @@ def _raw_stream(dev: int, *ts, stream=None):
                              f"{'the CPU' if dev < 0 else f'cuda:{dev}'}")
     if dev < 0:
         raise ValueError("the tensors must be on a CUDA device")
-    if torch._C._cuda_getDevice() != dev:
-        raise ValueError(f"tensors on cuda:{dev} but the current CUDA device is cuda:{torch.cuda.current_device()}; "
+    if _current_device() != dev:
+        raise ValueError(f"tensors on cuda:{dev} but the current CUDA device is cuda:{_current_device()}; "
                          "call under torch.cuda.device(...) of the tensors' device")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _current_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _rows(t: torch.Tensor, name: str, shape, dtype):
     """Rows [..., d] with a contiguous head dimension; returns the strides."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}; expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
+    if t.shape != shape or t.dtype is not dtype:
+        _expect(t, name, shape, dtype)
     s = t.stride()
     if s[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the head dimension must be contiguous")
-    return s[:-1]
+    return s
 
 
 def _rotate(q, k, rotary, positions, t0, q_out, k_out, flags, stream):
-    if q.dim() != 4 or (k is not None and k.dim() != 4):
-        raise ValueError("q and k must be [B,heads,T,d]")
     qn, dtype = q.shape, q.dtype
+    if len(qn) != 4:
+        raise ValueError("q must be [B,Hq,T,d]")
     B, Hq, T, d = qn
-    H = 0
     if q_out is None:
         q_out = torch.empty(qn, dtype=dtype, device=q.device)
-    qs, qos = _rows(q, "q", qn, dtype), _rows(q_out, "q_out", qn, dtype)
-    ks = kos = (0, 0, 0)
-    if k is not None:
-        H = k.shape[1]
-        kn = (B, H, T, d)
+    a, c = _rows(q, "q", qn, dtype), _rows(q_out, "q_out", qn, dtype)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        H, b, e, kp, kop = 0, _NO_STRIDE, _NO_STRIDE, 0, 0
+    else:
+        kn = k.shape
+        if len(kn) != 4 or kn[0] != B or kn[2] != T or kn[3] != d:
+            raise ValueError(f"k has shape {tuple(kn)}; expected [{B},H,{T},{d}]")
+        H = kn[1]
         if k_out is None:
             k_out = torch.empty(kn, dtype=dtype, device=q.device)
-        ks, kos = _rows(k, "k", kn, dtype), _rows(k_out, "k_out", kn, dtype)
-    elif k_out is not None:
-        raise ValueError("k_out without k")
+        b, e = _rows(k, "k", kn, dtype), _rows(k_out, "k_out", kn, dtype)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    pp = 0
     if positions is not None:
         _expect(positions, "positions", (B, T), torch.int64)
         _contig(positions)
-    desc = _PACK_ROTATE.pack(B, Hq, H, T, d, _dtype_code(q), flags, *qs, *ks, *qos, *kos)
+        pp = positions.data_ptr()
+    desc = _PACK_ROTATE.pack(B, Hq, H, T, d, _dtype_code(q), flags, a[0], a[1], a[2], b[0], b[1], b[2], c[0], c[1], c[2],
+                             e[0], e[1], e[2])
     s = _raw_stream(q.get_device(), k, q_out, k_out, positions, stream=stream)
-    st = _lib.tc_rotate(desc, rotary.ref, _addr(positions), int(t0), q.data_ptr(), _addr(k), q_out.data_ptr(),
-                        _addr(k_out), s)
+    st = _lib.tc_rotate(desc, rotary.ref, pp, t0, q.data_ptr(), kp, q_out.data_ptr(), kop, s)
     if st:
         raise TCError(st, "tc_rotate")
     return q_out, k_out
+
+
+_NO_STRIDE = (0, 0, 0)
 
 
 def rotate(q: torch.Tensor, k: Optional[torch.Tensor], rotary: Rotary, *,
@@ -923,23 +932,27 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, rotary:
     B, H, d, T = cache.B, cache.H, cache.d, k.shape[2]
     kn = (B, H, T, d)
     ks, vs = _rows(k, "k", kn, cache.dtype), _rows(v, "v", kn, cache.dtype)
-    qs, Hq = (0, 0, 0), 0
+    qs, Hq = _NO_STRIDE, 0
     if q is not None:
         if q.dim() != 4:
             raise ValueError("q must be [B,Hq,T,d]")
         Hq = q.shape[1]
-        qs = _rows(q, "q", (B, Hq, T, d), cache.dtype)
+        qn = (B, Hq, T, d)
+        qs = _rows(q, "q", qn, cache.dtype)
         if q_out is None:
-            q_out = torch.empty((B, Hq, T, d), dtype=q.dtype, device=q.device)
-        _expect(q_out, "q_out", (B, Hq, T, d), cache.dtype)
+            q_out = torch.empty(qn, dtype=q.dtype, device=q.device)
+        elif q_out.shape != qn or q_out.dtype is not cache.dtype:
+            _expect(q_out, "q_out", qn, cache.dtype)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _expect(counts, "counts", (B,), torch.int64)
-    _expect(mass, "mass", (B, H, T), torch.float32)
+    if counts is not None:
+        _expect(counts, "counts", (B,), torch.int64)
+    if mass is not None:
+        _expect(mass, "mass", (B, H, T), torch.float32)
     _contig(counts, mass, q_out)
     s = _raw_stream(cache.dev, k, v, q, q_out, counts, mass, stream=stream)
-    a = _PACK_APPEND.pack(T, Hq, _addr(q), k.data_ptr(), v.data_ptr(), *qs, *ks, *vs, _addr(counts), _addr(mass),
-                          _addr(q_out))
+    a = _PACK_APPEND.pack(T, Hq, _addr(q), k.data_ptr(), v.data_ptr(), *qs[:3], *ks[:3], *vs[:3], _addr(counts),
+                          _addr(mass), _addr(q_out))
     st = _lib.tc_cache_append(cache.ref, None if rotary is None else rotary.ref, a, s)
     if st:
         raise TCError(st, "tc_cache_append")
@@ -960,14 +973,16 @@ def cache_attend(cache: PagedCache, q: torch.Tensor, *, g: Optional[torch.Tensor
     accumulate adds each pair's weight to the cache's mass.  Returns y
     [B,Hq,d]; rows that are empty (negative length) are not written."""
     Hq = _query_heads(cache, q)
-    _expect(g, "g", (Hq,), torch.float32)
-    if g is not None and cache.A is None:
-        raise ValueError("g reads the memory, but the cache has none")
+    if g is not None:
+        _expect(g, "g", (Hq,), torch.float32)
+        if cache.A is None:
+            raise ValueError("g reads the memory, but the cache has none")
     if accumulate and cache.mass is None:
         raise ValueError("accumulate needs a cache with mass")
     if y is None:
         y = torch.empty_like(q)
-    _expect(y, "y", q.shape, cache.dtype)
+    elif y.shape != q.shape or y.dtype is not cache.dtype:
+        _expect(y, "y", q.shape, cache.dtype)
     flags = TC_CACHE_ACCUMULATE if accumulate else 0
     n = 0 if workspace is not None else _lib.tc_cache_attend_workspace_size(cache.ref, Hq, flags)
     workspace, room = _workspace(n, "tc_cache_attend_workspace_size", workspace, cache.device)
@@ -1025,21 +1040,23 @@ def cache_step(cache: PagedCache, q: torch.Tensor, k: torch.Tensor, v: torch.Ten
     Hq = _query_heads(cache, q)
     kn = (cache.B, cache.H, cache.d)
     qs, ks, vs = _rows(q, "q", (cache.B, Hq, cache.d), cache.dtype), _rows(k, "k", kn, cache.dtype), _rows(v, "v", kn, cache.dtype)
-    _expect(g, "g", (Hq,), torch.float32)
-    if g is not None and cache.A is None:
-        raise ValueError("g reads the memory, but the cache has none")
+    if g is not None:
+        _expect(g, "g", (Hq,), torch.float32)
+        if cache.A is None:
+            raise ValueError("g reads the memory, but the cache has none")
     if cache.mass is None:
         raise ValueError("a step needs a cache with mass and pos")
     if y is None:
         y = torch.empty((cache.B, Hq, cache.d), dtype=cache.dtype, device=q.device)
-    _expect(y, "y", q.shape, cache.dtype)
+    elif y.shape != q.shape or y.dtype is not cache.dtype:
+        _expect(y, "y", q.shape, cache.dtype)
     flags = TC_CACHE_ACCUMULATE if accumulate else 0
     n = 0 if workspace is not None else _lib.tc_cache_step_workspace_size(cache.ref, Hq, flags)
     workspace, room = _workspace(n, "tc_cache_step_workspace_size", workspace, cache.device)
     _contig(g, y)
     s = _raw_stream(cache.dev, q, k, v, g, y, workspace, stream=stream)
-    a = _PACK_STEP.pack(Hq, q.data_ptr(), k.data_ptr(), v.data_ptr(), *qs, *ks, *vs, _addr(g), y.data_ptr(), int(budget),
-                        int(recent), flags)
+    a = _PACK_STEP.pack(Hq, q.data_ptr(), k.data_ptr(), v.data_ptr(), *qs[:2], *ks[:2], *vs[:2], _addr(g), y.data_ptr(),
+                        int(budget), int(recent), flags)
     st = _lib.tc_cache_step(cache.ref, None if rotary is None else rotary.ref, a, workspace.data_ptr(), room, s)
     if st:
         raise TCError(st, "tc_cache_step")
