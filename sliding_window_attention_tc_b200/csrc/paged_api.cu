@@ -353,7 +353,6 @@ tc_status tc_cache_evict(const tc_paged_cache *c, int64_t budget, int64_t recent
     p.row_len = reinterpret_cast<int64_t *>(ws + room.row_len);
     p.sort_ws = reinterpret_cast<unsigned char *>(ws + room.sort);
     p.Hq = (int)c->H;
-    p.wait_ns = api_wait_limit_ns();
     const cudaError_t e = launch_cache_evict(p, c->dtype, (int)c->d, sms, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? TC_OK : TC_ERR_CUDA;
 }
@@ -396,7 +395,6 @@ tc_status tc_cache_step(const tc_paged_cache *c, const tc_rotary *rotary, const 
     e.budget = a->budget;
     e.recent = a->recent;
     e.row_len = reinterpret_cast<int64_t *>(ws + room.row_len);
-    e.wait_ns = api_wait_limit_ns();
     e.q = a->q;
     e.k_new = a->k;
     e.v_new = a->v;

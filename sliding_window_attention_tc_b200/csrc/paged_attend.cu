@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kFThreads) attend_f32_kernel(const __grid_cons
     constexpr int LPK = D / 4;                 // lanes per pair
     constexpr int KPW = 32 / LPK;              // pairs a warp loads at once
     constexpr int NG = kFWarps * KPW;           // groups of lanes with statistics of their own
-    constexpr int BATCH = 4;                   // loads of keys in flight per lane (and of values)
+    constexpr int BATCH = GT <= 2 ? 8 : 4;     // loads of keys in flight per lane (and of values)
     __shared__ float s_m[NG][GT], s_l[NG][GT];
     __shared__ __align__(16) float s_o[NG][GT][D];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

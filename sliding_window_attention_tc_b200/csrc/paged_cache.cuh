@@ -67,7 +67,6 @@ struct EvictParams {
     float *memo;             // [B,H,slices,G,d] q A by slices of A's rows; null: no read
     int Hq;
     RotaryTable table;
-    unsigned long long wait_ns;
 };
 // Blocks a head's A is cut over in a step's first kernel (and p.memo's slices).
 int evict_slices(int64_t BH, int d, int num_sms);
