@@ -450,9 +450,9 @@ TC_API tc_status tc_rotate(const tc_rotate_desc *desc, const tc_rotary *rotary,
  * Row b holds len[b] pairs in slots 0 .. len[b]-1; slot s lives in page
  * table[b][s / page], at row s mod page of that page, the same for every head.
  * Slots carry no order: a pair's position is in pos (and, rotated, in its key).
- * All arrays are caller-owned device memory, updated in place.  Rows must not
- * share pages, except that rows which are only attended to without
- * TC_CACHE_ACCUMULATE may share any.
+ * All arrays are caller-owned device memory, updated in place.  No page may be
+ * named twice, by two rows or by one, except that rows which are only attended
+ * to without TC_CACHE_ACCUMULATE may share any.
  *   1 <= B <= 65535; 1 <= H; B H <= 2^20; d in {16, 32, 64, 128} (d_k = d_v);
  *   page a multiple of 16, at most 4096; 1 <= max_pages;
  *   n_pages H page < 2^31; max_pages page <= 2^24; B max_pages page <= 2^36.
@@ -508,7 +508,8 @@ TC_API tc_status tc_cache_append(const tc_paged_cache *cache, const tc_rotary *r
  * memory's read (Fig. 2 step (5)): for query head h, which reads key/value head
  * h / (Hq/H),
  *   p = softmax_j(<q,k_j>/sqrt(d)),  y = sum_j p_j v_j + sigmoid(g_h) q A.
- * A row that holds no pair gives the memory's read alone.  With
+ * A row that holds no pair (or whose scores are all -infinity) gives the
+ * memory's read alone.  With
  * TC_CACHE_ACCUMULATE mass_j grows by the sum of p_j over the heads that share
  * the key/value head.
  *   q, y [B,Hq,d] contiguous, Hq a multiple of H, Hq/H <= 128,
@@ -543,7 +544,9 @@ TC_API tc_status tc_cache_evict(const tc_paged_cache *cache, int64_t budget, int
  * query reads both.  For rows that held at most budget pairs these are the
  * results of tc_cache_append, tc_cache_evict and tc_cache_attend, in three
  * launches; a row above its budget (after a lower one was chosen) stays above
- * it by as much until tc_cache_evict is called.
+ * it by as much until tc_cache_evict is called.  The pair enters before one
+ * leaves: a row's table has room for len + 1 pairs, or the row is skipped with
+ * TC_ERR_DEVICE_BOUNDS.
  *   q [B,Hq,d], k, v [B,H,d]: not rotated (rotary NULL: used as they are);
  *   strides in elements of b and h (slices of a fused projection), the head
  *   dimension contiguous, the alignment of their type; y [B,Hq,d] contiguous.

@@ -755,9 +755,10 @@ def _addr(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.data_ptr()
 
 
-def _raw_stream(dev: int, *ts, stream=None):
+def _raw_stream(dev: int, *ts, stream=None, used=()):
     """The stream to launch on, for tensors that must all be on CUDA device
-    `dev`, the current one."""
+    `dev`, the current one.  `used`: what the call may have allocated itself,
+    on the current stream; the allocator learns that a given stream uses it."""
     for t in ts:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensor on {t.device}; the call's other tensors are on "
@@ -767,7 +768,12 @@ def _raw_stream(dev: int, *ts, stream=None):
     if _current_device() != dev:
         raise ValueError(f"tensors on cuda:{dev} but the current CUDA device is cuda:{_current_device()}; "
                          "call under torch.cuda.device(...) of the tensors' device")
-    return _current_stream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return _current_stream(dev)
+    for t in used:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
 
 
 def _rows(t: torch.Tensor, name: str, shape, dtype):
@@ -808,7 +814,7 @@ def _rotate(q, k, rotary, positions, t0, q_out, k_out, flags, stream):
         pp = positions.data_ptr()
     desc = _PACK_ROTATE.pack(B, Hq, H, T, d, _dtype_code(q), flags, a[0], a[1], a[2], b[0], b[1], b[2], c[0], c[1], c[2],
                              e[0], e[1], e[2])
-    s = _raw_stream(q.get_device(), k, q_out, k_out, positions, stream=stream)
+    s = _raw_stream(q.get_device(), k, q_out, k_out, positions, stream=stream, used=(q_out, k_out))
     st = _lib.tc_rotate(desc, rotary.ref, pp, t0, q.data_ptr(), kp, q_out.data_ptr(), kop, s)
     if st:
         raise TCError(st, "tc_rotate")
@@ -950,7 +956,7 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, rotary:
     if mass is not None:
         _expect(mass, "mass", (B, H, T), torch.float32)
     _contig(counts, mass, q_out)
-    s = _raw_stream(cache.dev, k, v, q, q_out, counts, mass, stream=stream)
+    s = _raw_stream(cache.dev, k, v, q, q_out, counts, mass, stream=stream, used=(q_out,))
     a = _PACK_APPEND.pack(T, Hq, _addr(q), k.data_ptr(), v.data_ptr(), *qs[:3], *ks[:3], *vs[:3], _addr(counts),
                           _addr(mass), _addr(q_out))
     st = _lib.tc_cache_append(cache.ref, None if rotary is None else rotary.ref, a, s)
@@ -987,7 +993,7 @@ def cache_attend(cache: PagedCache, q: torch.Tensor, *, g: Optional[torch.Tensor
     n = 0 if workspace is not None else _lib.tc_cache_attend_workspace_size(cache.ref, Hq, flags)
     workspace, room = _workspace(n, "tc_cache_attend_workspace_size", workspace, cache.device)
     _contig(q, g, y)
-    s = _raw_stream(cache.dev, q, g, y, workspace, stream=stream)
+    s = _raw_stream(cache.dev, q, g, y, workspace, stream=stream, used=(y, workspace))
     st = _lib.tc_cache_attend(cache.ref, Hq, q.data_ptr(), _addr(g), y.data_ptr(), flags, workspace.data_ptr(), room, s)
     if st:
         raise TCError(st, "tc_cache_attend")
@@ -1018,7 +1024,7 @@ def cache_evict(cache: PagedCache, budget: int, *, recent: int = 1,
         raise ValueError("eviction needs a cache with mass and pos")
     n = 0 if workspace is not None else _lib.tc_cache_evict_workspace_size(cache.ref)
     workspace, room = _workspace(n, "tc_cache_evict_workspace_size", workspace, cache.device)
-    s = _raw_stream(cache.dev, workspace, stream=stream)
+    s = _raw_stream(cache.dev, workspace, stream=stream, used=(workspace,))
     _check(_lib.tc_cache_evict(cache.ref, int(budget), int(recent), workspace.data_ptr(), room, s), "tc_cache_evict")
 
 
@@ -1054,7 +1060,7 @@ def cache_step(cache: PagedCache, q: torch.Tensor, k: torch.Tensor, v: torch.Ten
     n = 0 if workspace is not None else _lib.tc_cache_step_workspace_size(cache.ref, Hq, flags)
     workspace, room = _workspace(n, "tc_cache_step_workspace_size", workspace, cache.device)
     _contig(g, y)
-    s = _raw_stream(cache.dev, q, k, v, g, y, workspace, stream=stream)
+    s = _raw_stream(cache.dev, q, k, v, g, y, workspace, stream=stream, used=(y, workspace))
     a = _PACK_STEP.pack(Hq, q.data_ptr(), k.data_ptr(), v.data_ptr(), *qs[:2], *ks[:2], *vs[:2], _addr(g), y.data_ptr(),
                         int(budget), int(recent), flags)
     st = _lib.tc_cache_step(cache.ref, None if rotary is None else rotary.ref, a, workspace.data_ptr(), room, s)

@@ -43,7 +43,7 @@ __device__ __forceinline__ int64_t append_count(const AppendParams &p, int b, in
     if (len < 0) return -1;
     const int64_t n = p.counts ? p.counts[b] : p.T;
     bad = n < 0 || n > p.T || len + n > p.c.capacity() || len > p.c.capacity() || clock < 0 ||
-          clock + n > (int64_t(1) << 31);
+          clock > (int64_t(1) << 31) - n;
     if (!bad) bad = !block_pages_ok(p.c, b, len, len + n - 1);
     return bad ? -1 : n;
 }

@@ -472,3 +472,130 @@ def test_attend_wait_limit(cuda_device):
         tc.set_wait_limit_ns(0)
     check_y(tc.cache_attend(c, q.cuda()), *cpu.attend(q))
     assert tc.device_status() == 0
+
+
+def test_given_stream_keeps_the_calls_memory(cuda_device):
+    """What a call allocates for itself and hands to a stream it was given is not
+    dealt again while that stream still has the call before it."""
+    import sliding_window_attention_tc_b200 as tc
+    c, cpu = make([300, 40], d=64, H=2, seed=5)
+    q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(5)).bfloat16()
+    qd, side = q.cuda(), torch.cuda.Stream()
+    size = tc.cache_attend_workspace(c, 4).nbytes
+    torch.cuda.synchronize()
+    # the blocks the allocator would deal for a workspace, found by asking for one
+    x = torch.empty(size, dtype=torch.uint8, device="cuda")
+    at = x.data_ptr()
+    del x
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    y = tc.cache_attend(c, qd, stream=side)
+    again = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(t.data_ptr() != at for t in again)
+    torch.cuda.synchronize()
+    check_y(y, *cpu.attend(q))
+    assert tc.device_status() == 0
+
+
+@pytest.mark.parametrize("clock", [2 ** 31 - 4, 2 ** 62, 2 ** 63 - 1, -1])
+def test_clocks_past_the_last_position(cuda_device, clock):
+    """Tokens whose positions would pass 2^31 - 1 do not enter, however far the
+    clock is; a step refuses a clock that is there."""
+    import sliding_window_attention_tc_b200 as tc
+    c, cpu = make([20, 20], d=64, H=2, seed=6)
+    c.clocks[1] = clock
+    k, v = torch.randn(2, 2, 2, 5, 64, generator=torch.Generator().manual_seed(6)).bfloat16()
+    tc.cache_append(c, k.cuda(), v.cuda())
+    assert tc.device_status() == 5
+    assert c.lens.tolist() == [25, 20] and c.clocks.tolist() == [30, clock]
+    pg, sl = cpu.at(1, range(20, 25))
+    assert torch.equal(torch.isnan(c.k_pages.cpu()[pg, :, sl]), torch.isnan(cpu.k[pg, :, sl]))
+    if clock == 2 ** 31 - 4:
+        return
+    q = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    tc.cache_step(c, q, q, q, 64)
+    assert tc.device_status() == 5 and c.lens.tolist() == [26, 20]
+
+
+def test_step_needs_room_for_one_more(cuda_device):
+    """The pair enters before one leaves: a row whose table is full is left as it
+    is, the others go on."""
+    import sliding_window_attention_tc_b200 as tc
+    c, cpu = make([64, 63], d=64, H=2, seed=7, room=0)
+    assert c.table.shape[1] * 16 == 64
+    q = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    y = torch.full_like(q, 3.0)
+    tc.cache_step(c, q, q, q, 64, y=y)
+    assert tc.device_status() == 5
+    assert c.lens.tolist() == [64, 64] and c.clocks.tolist() == [cpu.clocks[0], cpu.clocks[1] + 1]
+    assert torch.all(y[0] == 3.0) and not torch.any(y[1] == 3.0)
+    pg, sl = cpu.at(0, range(64))
+    assert torch.equal(c.v_pages.cpu()[pg, :, sl], cpu.v[pg, :, sl])
+
+
+def test_padded_prompts(cuda_device):
+    """A padded batch whose rows have no, one, some or all of the tokens, in more
+    than one block a row; NaN in the padding."""
+    import sliding_window_attention_tc_b200 as tc
+    T, counts = 150, [0, 1, 77, 150, 8, 9, 5]
+    for dtype, d, spec in (("f32", 64, dict(rot=64)), ("bf16", 128, dict(rot=64)), ("bf16", 16, dict(rot=16))):
+        c, cpu = make([0, 3, 16, 5, 0, 7, -1], d=d, H=3, dtype=dtype, seed=d, room=160)
+        gen = torch.Generator().manual_seed(d)
+        k, v = torch.randn(2, 7, 3, T, d, generator=gen).to(DT[dtype])
+        q = torch.randn(7, 6, T, d, generator=gen).to(DT[dtype])
+        for b, n in enumerate(counts):
+            for x in (k, v, q):
+                x[b, :, n:] = math.nan
+        q_out = torch.full_like(q, 3.0).cuda()
+        tc.cache_append(c, k.cuda(), v.cuda(), rotary=tc.Rotary(**spec), q=q.cuda(), counts=torch.tensor(counts).cuda(), q_out=q_out)
+        want = cpu.append(k, v, spec, q=q, counts=counts)
+        same_state(c, cpu, exact_keys=False)
+        eps = torch.finfo(DT[dtype]).eps / 2
+        for b, n in enumerate(counts):
+            n = n if b < 6 else 0
+            got = q_out[b].cpu().double()
+            assert torch.all(got[:, n:] == 3.0)  # rows past a row's tokens are not written
+            assert torch.all((got[:, :n] - want[b, :, :n]).abs() <= eps * want[b, :, :n].abs() + 2.0 ** -20 * 10)
+    assert tc.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_offsets_past_32_bits(cuda_device, dtype):
+    """The same calls on a small pool and on the last pages of one of more than
+    2^31 elements: the same bits."""
+    import sliding_window_attention_tc_b200 as tc
+    H, G, d, page, B, width = 2, 2, 128, 64, 3, 4
+    far = 2 ** 31 // (H * page * d) + 7  # pages whose elements pass 2^31
+    perm = torch.randperm(B * width, generator=torch.Generator().manual_seed(1)).view(B, width).int()
+    lam, eta = torch.tensor([0.9, 0.97]).cuda(), torch.tensor([0.5, 0.7]).cuda()
+    caches = []
+    for base in (0, far):
+        n = base + B * width
+        pool = [torch.empty(n, H, page, d, dtype=DT[dtype], device="cuda") for _ in range(2)]
+        c = tc.PagedCache(*pool, (perm + base).cuda(), torch.zeros(B, dtype=torch.int64).cuda(), torch.zeros(B, dtype=torch.int64).cuda(),
+                          mass=torch.zeros(n, H, page).cuda(), pos=torch.zeros(n, H, page, dtype=torch.int32).cuda(),
+                          A=torch.zeros(B, H, d, d).cuda(), lam=lam, eta=eta)
+        for t in (*pool, c.mass, c.pos):
+            t[base:].zero_()
+        caches.append((c, base))
+    gen = torch.Generator().manual_seed(2)
+    r = tc.Rotary(d)
+    k, v = torch.randn(2, B, H, 150, d, generator=gen).to(DT[dtype]).cuda()
+    w = torch.rand(B, H, 150, generator=gen).cuda()
+    q = torch.randn(B, H * G, d, generator=gen).to(DT[dtype]).cuda()
+    g = torch.randn(H * G, generator=gen).cuda()
+    out = []
+    for c, base in caches:
+        ys = []
+        tc.cache_append(c, k, v, rotary=r, mass=w)
+        ys.append(tc.cache_attend(c, q, g=g, accumulate=True))
+        tc.cache_evict(c, 100, recent=8)
+        ys.append(tc.cache_attend(c, q, g=g))
+        tc.cache_append(c, k[:, :, :1], v[:, :, :1], rotary=r)
+        tc.cache_evict(c, 100, recent=8)
+        for i in range(3):
+            ys.append(tc.cache_step(c, q, k[:, :, i], v[:, :, i], 100, rotary=r, g=g))
+        out.append(ys + [c.A, c.lens, c.clocks] + [t[base:] for t in (c.k_pages, c.v_pages, c.mass, c.pos)])
+    for a, b in zip(*out):
+        assert torch.equal(a, b) and not torch.any(torch.isnan(a.double()))
+    assert tc.device_status() == 0
