@@ -667,68 +667,140 @@ __device__ __forceinline__ uint32_t *sort_slots(uint32_t *order, uint32_t *other
     return swapped ? other : order;
 }
 
-// The same order, for weights that spread: the slots are counted into buckets
-// by weight (the bits of a float are its logarithm, so even steps of the bits
-// spread weights of any scale; zeros, of which there may be many, have a bucket of
-// their own; protected pairs theirs behind the others), and each finds its place
-// among its bucket's few by comparing.  False, and nothing done, when that would
-// be more than kCompareMost comparisons a slot.  lo, hi: the least weight above zero and the
-// greatest, as ordered bits; none below zero.
+// The same order (of its first m places: the others are not defined), for weights
+// that differ: the slots are counted into buckets by weight (the bits of a float
+// are its logarithm, so even steps of the bits spread weights of any scale; zeros
+// have a bucket of their own; protected pairs theirs behind the others), and each
+// finds its place among its bucket's few by comparing.  Buckets of more than
+// kCompareMost (tokens that nothing has attended to yet, for one) are cut into
+// buckets again, by position where all their weights are equal.  (2559 pairs, the
+// kernel over 96 heads of d = 64: 62 us; with 2047 zeros among them 65 us, 88 sorted
+// by digits; with a quarter of them equal 67 us, 83.)  False, and nothing done, where
+// pairs are alike in both or too many buckets are large.  lo, hi: the least weight
+// above zero and the greatest, as ordered bits; none below zero.
 constexpr int kBuckets = 4096;     // plain and protected; 16-bit counters, two to a word
 constexpr int kCompareMost = 64;
+constexpr int kMostLarge = 8;
 
-__device__ bool bucket_sort(uint32_t *order, uint32_t *other, const uint32_t *weight, const uint32_t *place, int n, uint32_t lo, uint32_t hi,
-                            uint32_t *words, int *scan) {
+// The counters of a thread (8, in 4 words), and as the places where their buckets begin.
+__device__ __forceinline__ void bucket_begins(uint32_t *words, int *scan, uint32_t (&c)[kBuckets / kBulkThreads],
+                                              uint32_t (&at)[kBuckets / kBulkThreads]) {
+    constexpr int N = kBuckets / kBulkThreads;
+    static_assert(N == 8, "one vector of words");
+    uint4 *mine = reinterpret_cast<uint4 *>(words) + threadIdx.x;
+    const uint4 w = *mine;
+    const uint32_t x[N] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16, w.z & 0xffffu, w.z >> 16, w.w & 0xffffu, w.w >> 16};
+    int sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        c[i] = x[i];
+        sum += (int)x[i];
+    }
+    uint32_t begin = (uint32_t)block_scan(sum, scan, &total);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        at[i] = begin;
+        begin += x[i];
+    }
+    *mine = make_uint4(at[0] | at[1] << 16, at[2] | at[3] << 16, at[4] | at[5] << 16, at[6] | at[7] << 16);
+}
+__device__ __forceinline__ uint32_t half_word(const uint32_t *words, uint32_t i) { return words[i / 2] >> (i % 2 * 16) & 0xffffu; }
+
+// words: 2 x kBuckets / 2 counters and 32 more.
+__device__ bool bucket_sort(uint32_t *order, uint32_t *other, const uint32_t *weight, const uint32_t *place, int n, int m, uint32_t lo,
+                            uint32_t hi, uint32_t *words, int *scan) {
+    constexpr int N = kBuckets / kBulkThreads;
     const int tid = threadIdx.x;
+    uint32_t *sub = words + kBuckets / 2, *large = sub + kBuckets / 2, *ends = large + 16;
     const int shift = max(0, 32 - __clz(hi - lo) - 11);  // (hi - lo) >> shift below 2048
     auto bucket = [&](uint32_t s) {
         const uint32_t v = weight[s];
         return (place[s] >> 31) * (kBuckets / 2) + (v == 0x80000000u ? 0u : min(1u + ((v - lo) >> shift), (uint32_t)kBuckets / 2 - 1));
     };
+    auto next_place = [](uint32_t *table, uint32_t b) { return atomicAdd(table + b / 2, 1u << (b % 2 * 16)) >> (b % 2 * 16) & 0xffffu; };
+    // how many of list[0 .. count) come before slot s
+    auto rank = [&](const uint32_t *list, uint32_t count, uint32_t s) {
+        const uint32_t v = weight[s], z = place[s];
+        uint32_t r = 0;
+#pragma unroll 4
+        for (uint32_t j = 0; j < count; ++j) {
+            const uint32_t x = list[j], vx = weight[x], zx = place[x];  // (within a bucket z's top bits agree)
+            r += vx < v || (vx == v && (zx < z || (zx == z && x < s)));
+        }
+        return r;
+    };
     for (int x = tid; x < kBuckets / 2; x += kBulkThreads) words[x] = 0;
+    if (tid == 0) large[0] = 0;
     __syncthreads();
-    for (int s = tid; s < n; s += kBulkThreads) {
-        const uint32_t b = bucket(s);
-        atomicAdd(words + b / 2, 1u << (b % 2 * 16));
-    }
+    for (int s = tid; s < n; s += kBulkThreads) next_place(words, bucket(s));
     __syncthreads();
-    constexpr int PER = kBuckets / 2 / kBulkThreads;  // words of a thread
-    static_assert(PER == 4, "one vector");
-    uint4 w = reinterpret_cast<const uint4 *>(words)[tid];
-    uint32_t c[2 * PER] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16, w.z & 0xffffu, w.z >> 16, w.w & 0xffffu, w.w >> 16};
-    int sum = 0, compared = 0, total;
+    uint32_t c[N], at[N];
+    bucket_begins(words, scan, c, at);
 #pragma unroll
-    for (int i = 0; i < 2 * PER; ++i) {
-        compared += (int)(c[i] * c[i]);  // below 2^27 in all
-        sum += (int)c[i];
-    }
-    block_scan(compared, scan, &total);
-    if (total > kCompareMost * n) return false;
-    uint32_t at = (uint32_t)block_scan(sum, scan, &total);
-#pragma unroll
-    for (int i = 0; i < 2 * PER; ++i) {
-        const uint32_t x = c[i];
-        c[i] = at;
-        at += x;
-    }
-    reinterpret_cast<uint4 *>(words)[tid] = make_uint4(c[0] | c[1] << 16, c[2] | c[3] << 16, c[4] | c[5] << 16, c[6] | c[7] << 16);
+    for (int i = 0; i < N; ++i)
+        if (c[i] > kCompareMost && (int)at[i] < m) {
+            const uint32_t x = atomicAdd(large, 1u);
+            if (x < kMostLarge) large[1 + x] = at[i] | (at[i] + c[i]) << 16;
+        }
     __syncthreads();
-    for (int s = tid; s < n; s += kBulkThreads) {
-        const uint32_t b = bucket(s);
-        other[(atomicAdd(words + b / 2, 1u << (b % 2 * 16)) >> (b % 2 * 16)) & 0xffffu] = s;
-    }
+    if (large[0] > kMostLarge) return false;
+    for (int s = tid; s < n; s += kBulkThreads) other[next_place(words, bucket(s))] = s;
     __syncthreads();
     // the counters are the buckets' ends now
     for (int i = tid; i < n; i += kBulkThreads) {
-        const uint32_t s = other[i], b = bucket(s), v = weight[s], z = place[s];
-        const uint32_t begin = b ? words[(b - 1) / 2] >> ((b - 1) % 2 * 16) & 0xffffu : 0u, end = words[b / 2] >> (b % 2 * 16) & 0xffffu;
-        uint32_t to = begin;
-#pragma unroll 4
-        for (uint32_t j = begin; j < end; ++j) {
-            const uint32_t x = other[j], vx = weight[x], zx = place[x];  // (within a bucket z's top bits agree)
-            to += vx < v || (vx == v && (zx < z || (zx == z && x < s)));
+        const uint32_t s = other[i], b = bucket(s), begin = b ? half_word(words, b - 1) : 0u, end = half_word(words, b);
+        if ((int)begin < m && end - begin <= kCompareMost) order[begin + rank(other + begin, end - begin, s)] = s;
+    }
+    for (uint32_t l = 0; l < large[0]; ++l) {
+        const uint32_t begin = large[1 + l] & 0xffffu, end = large[1 + l] >> 16;
+        for (int x = tid; x < kBuckets / 2; x += kBulkThreads) sub[x] = 0;
+        if (tid < 4) ends[tid] = tid % 2 ? 0u : ~0u;  // weights' least and greatest, positions'
+        __syncthreads();
+        uint32_t e[4] = {~0u, 0u, ~0u, 0u};
+        for (uint32_t i = begin + tid; i < end; i += kBulkThreads) {
+            const uint32_t s = other[i];
+            e[0] = min(e[0], weight[s]);
+            e[1] = max(e[1], weight[s]);
+            e[2] = min(e[2], place[s]);
+            e[3] = max(e[3], place[s]);
         }
-        order[to] = s;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            e[x] = x % 2 ? __reduce_max_sync(0xffffffffu, e[x]) : __reduce_min_sync(0xffffffffu, e[x]);
+            if (tid % 32 == 0) x % 2 ? atomicMax(ends + x, e[x]) : atomicMin(ends + x, e[x]);
+        }
+        __syncthreads();
+        const bool equal = ends[0] == ends[1];
+        const uint32_t *key = equal ? place : weight, least = equal ? ends[2] : ends[0], range = (equal ? ends[3] : ends[1]) - least;
+        const int cut = max(0, 32 - __clz(range) - 12);  // range >> cut below 4096
+        for (uint32_t i = begin + tid; i < end; i += kBulkThreads) next_place(sub, (key[other[i]] - least) >> cut);
+        __syncthreads();
+        bucket_begins(sub, scan, c, at);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (c[i] > kCompareMost && (int)(begin + at[i]) < m) {  // again; not where all are alike
+                const uint32_t x = range ? atomicAdd(large, 1u) : kMostLarge;
+                if (x < kMostLarge) large[1 + x] = (begin + at[i]) | (begin + at[i] + c[i]) << 16;
+                else large[0] = kMostLarge + 1;
+            }
+        __syncthreads();
+        if (large[0] > kMostLarge) {
+            for (int s = tid; s < n; s += kBulkThreads) order[s] = s;
+            __syncthreads();
+            return false;
+        }
+        for (uint32_t i = begin + tid; i < end; i += kBulkThreads) {
+            const uint32_t s = other[i];
+            order[begin + next_place(sub, (key[s] - least) >> cut)] = s;
+        }
+        __syncthreads();
+        for (uint32_t i = begin + tid; i < end; i += kBulkThreads) {
+            const uint32_t s = order[i], x = (key[s] - least) >> cut, first = begin + (x ? half_word(sub, x - 1) : 0u),
+                           count = begin + half_word(sub, x) - first;
+            other[count > kCompareMost ? i : first + rank(order + first, count, s)] = s;
+        }
+        __syncthreads();
+        for (uint32_t i = begin + tid; i < end; i += kBulkThreads) order[i] = other[i];
     }
     __syncthreads();
     return true;
@@ -952,11 +1024,11 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
             // the same addresses, from the block's own shared memory, so that they
             // are accessed as such
             uint32_t *o = reinterpret_cast<uint32_t *>(dyn), *w = reinterpret_cast<uint32_t *>(dyn + order_room(n_cap));
-            const bool spread = w_min >= 0x80000000u && w_lo < w_hi;  // no weight below zero, two above
+            const bool spread = w_min >= 0x80000000u && w_differ;  // no weight below zero, two values
             auto sort = [&](auto items) {
                 return sort_slots<decltype(items)::value>(o, w + 2 * n_cap, w, w + n_cap, n, by_place, w_differ, z_differ, w + 3 * n_cap, s_total, s_base);
             };
-            from = spread && bucket_sort(o, w + 2 * n_cap, w, w + n_cap, n, w_lo, w_hi, w + 3 * n_cap, s_scan) ? o
+            from = spread && bucket_sort(o, w + 2 * n_cap, w, w + n_cap, n, m, w_lo, w_hi, w + 3 * n_cap, s_scan) ? o
                    : n <= kBulkThreads     ? sort(std::integral_constant<int, 1>())
                    : n <= 3 * kBulkThreads ? sort(std::integral_constant<int, 3>())
                    : n <= 5 * kBulkThreads ? sort(std::integral_constant<int, 5>())

@@ -291,6 +291,35 @@ def test_evict_odd_weights(cuda_device):
             same_state(c, cpu, A_terms=40)
 
 
+@pytest.mark.parametrize("kind", ["zeros", "zeros and one value", "two groups", "ten groups", "close", "equal positions", "behind"])
+def test_evict_crowded_weights(cuda_device, kind):
+    """Weights that crowd: many zeros, groups of equal ones (more of them than are
+    taken apart one by one, too), neighbours far from the rest, equal positions."""
+    import sliding_window_attention_tc_b200 as tc
+    n = 1500
+    c, cpu = make([n, 700, n], d=16, H=2, dtype="f32", seed=len(kind), room=0)
+    gen = torch.Generator().manual_seed(len(kind))
+    for b in range(3):
+        held = cpu.lens[b]
+        pg, sl = cpu.at(b, range(held))
+        i = torch.arange(held)
+        rare = torch.exp(4 * torch.randn(held, generator=gen))
+        w = {"zeros": torch.where(i % 10 == 3, rare, 0.0), "zeros and one value": (i % 4 == 1) * 2.5,
+             "two groups": torch.where(i % 3 == 0, 0.25, torch.where(i % 3 == 1, 3.0, rare)),
+             "ten groups": 2.0 ** (i % 10), "close": torch.where(i % 7 == 0, rare * 1e20, 1.0 + (i * 977 % held) * 2.0 ** -23),
+             "equal positions": torch.where(i % 5 == 0, rare, 7.0), "behind": torch.where(i % 2 == 0, 1e-3 * rare, 1e30)}[kind].float()
+        for x in (c.mass, cpu.mass):
+            x[pg.to(x.device), :, sl.to(x.device)] = w[:, None].to(x)
+        if kind == "equal positions":
+            for x in (c.pos, cpu.pos):
+                x[pg.to(x.device), :, sl.to(x.device)] = (i // 200)[:, None].to(x)
+    for budget in (1100, 640, 300):
+        tc.cache_evict(c, budget, recent=40)
+        cpu.evict(budget, 40)
+        same_state(c, cpu, A_terms=n)
+    assert tc.device_status() == 0
+
+
 def test_evict_many_pairs_at_once(cuda_device):
     """More pairs than are sorted in shared memory, and the same just below."""
     import sliding_window_attention_tc_b200 as tc
