@@ -490,7 +490,10 @@ __global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_
 constexpr int kBulkThreads = 512;
 constexpr int kBulkWarps = kBulkThreads / 32;
 constexpr int kSortMax = 8192;   // pairs sorted in shared memory (16 bytes each)
-constexpr int kPickMax = 32;     // pairs picked one after the other instead (rows of up to 32 * 512)
+// Pairs picked one after the other instead (rows of up to 32 * 512): of 96 heads
+// of 512 pairs and more, 8 leave in 24.3 us picked and in 27.0 sorted, 32 in 34.0
+// and 27.8; of 8 heads of 8000, 2 in 24.4 and 28.6, 32 in 43.9 and 32.8.
+constexpr int kPickMax = 10;
 
 // lambda^j for j >= 0 to float32's precision: the exponent in 64 bits, its
 // fraction to exp2f.
@@ -1312,7 +1315,9 @@ template <typename T, int D>
 cudaError_t launch_bulk_sl(const EvictParams &p, int slices, cudaStream_t s) {
     if constexpr (D >= 64)
         if (slices == 4) return launch_bulk<T, D, 4>(p, s);
-    return slices >= 2 ? launch_bulk<T, D, 2>(p, s) : launch_bulk<T, D, 1>(p, s);
+    if constexpr (D >= 32)
+        if (slices == 2) return launch_bulk<T, D, 2>(p, s);
+    return launch_bulk<T, D, 1>(p, s);
 }
 
 template <typename T>
@@ -1337,14 +1342,6 @@ cudaError_t launch_one_d(const EvictParams &p, int d, int slices, cudaStream_t s
     return cudaErrorInvalidValue;
 }
 
-// Slices a head's A is cut into, one block of a cluster each, of 16 rows at
-// least: more while the device has room for them.
-int slices_for(int64_t BH, int d, int most, int num_sms) {
-    int slices = 1;
-    while (slices * 2 <= d / 16 && slices < most && BH * slices * 2 <= 2 * num_sms) slices *= 2;
-    return slices;
-}
-
 }  // namespace
 
 cudaError_t launch_cache_append(const AppendParams &p, tc_dtype dtype, cudaStream_t s) {
@@ -1352,6 +1349,8 @@ cudaError_t launch_cache_append(const AppendParams &p, tc_dtype dtype, cudaStrea
     const int64_t es = dtype == TC_BF16 ? 2 : 4;
     const int vec = (int)(16 / es);
     const int64_t qn[3] = {p.c.B, p.Hq, p.T}, kn[3] = {p.c.B, p.c.H, p.T};
+    // 16-byte vectors where addresses and strides allow (2047 tokens for 8 rows, 12
+    // heads of d = 64, bf16: 23 us; element by element 62)
     const bool wide = p.table.rot % (2 * vec) == 0 && rows_aligned16(p.k, p.ks, kn, es) &&
                       rows_aligned16(p.v, p.vs, kn, es) && (!p.q || rows_aligned16(p.q, p.qs, qn, es));
     if (dtype == TC_BF16)
@@ -1359,11 +1358,20 @@ cudaError_t launch_cache_append(const AppendParams &p, tc_dtype dtype, cudaStrea
     return wide ? launch_append_vec<float, 4>(p, s) : launch_append_vec<float, 1>(p, s);
 }
 
-int evict_slices(int64_t BH, int d, int num_sms) { return slices_for(BH, d, 4, num_sms); }
+// Slices a head's A is cut into, one block of a cluster each: where A is large,
+// 2 or 4 while the device has room for them.  (A step of one row of 2048 pairs, 8
+// heads for 64, d = 128: 21.2 us with 4 slices, 23.3 with one; an eviction from 12
+// heads of d = 64: 8.2 us with 4 slices, 7.6 with one.)
+int evict_slices(int64_t BH, int d, int num_sms) {
+    return d < 128 ? 1 : BH * 4 <= 2 * num_sms ? 4 : BH * 2 <= 2 * num_sms ? 2 : 1;
+}
 
 namespace {
 // Blocks that share a head's pairs: 1, 2 or 4 (2 for the narrow heads, whose sums
 // are short), while all still run at once: two on an SM up to d = 64, one at 128.
+// 2047 of 2559 pairs: 12 heads of d = 64 with 4 blocks 37 us, with one 60; 8 of d =
+// 128 with 4 blocks 54 us, with one 124; 96 of d = 64 with 2 blocks 65 us, with one
+// 93, with 4 (in two waves) 83.
 int bulk_slices(int64_t BH, int d, int num_sms) {
     const int64_t room = (int64_t)(d <= 64 ? 2 : 1) * num_sms;
     return BH * 4 <= room && d >= 64 ? 4 : BH * 2 <= room && d >= 32 ? 2 : 1;

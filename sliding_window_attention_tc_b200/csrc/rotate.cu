@@ -65,7 +65,9 @@ cudaError_t launch_vec(const RotateParams &p, int num_sms, cudaStream_t s) {
     const int64_t units = p.B * p.T * chunks;
     if (units == 0) return cudaSuccess;
     // few tokens: the heads are split too, at the price of forming the angles
-    // again, until every SM has a full set of threads
+    // again, until every SM has a full set of threads (32 + 8 heads of d = 128, 512
+    // tokens: 4.3 us, unsplit 10.0; 12 + 12 heads of d = 64, 32768 tokens: 33.1 us
+    // unsplit, as the rule has it, 34.5 split as far as it goes)
     const int64_t want = ((int64_t)num_sms * 2048 + units - 1) / units;
     const int most = (heads + kRotUnroll - 1) / kRotUnroll;
     const int split = (int)(want < most ? want : most);
@@ -113,6 +115,8 @@ cudaError_t launch_rotate(const RotateParams &p, tc_dtype dtype, int num_sms, cu
     const int64_t es = dtype == TC_BF16 ? 2 : 4;
     const int vec = (int)(16 / es);
     const int64_t qn[3] = {p.B, p.Hq, p.T}, kn[3] = {p.B, p.H, p.T};
+    // 16-byte vectors where sizes, addresses and strides allow (the LM shape's q and
+    // k: 33 us; element by element 66; in float32, half the tokens, 33 and 42)
     bool wide = p.d % vec == 0 && p.table.rot % (2 * vec) == 0 && rows_aligned16(p.q, p.qs, qn, es) &&
                 rows_aligned16(p.q_out, p.qos, qn, es);
     if (p.H) wide = wide && rows_aligned16(p.k, p.ks, kn, es) && rows_aligned16(p.k_out, p.kos, kn, es);

@@ -252,7 +252,7 @@ def test_evict(cuda_device, dtype, d, H, held, budget, recent):
     same_state(c, cpu, A_terms=max(held))
 
 
-@pytest.mark.parametrize("m", [2, 3, 31, 32, 33, 64])
+@pytest.mark.parametrize("m", [2, 3, 9, 10, 11, 12, 33, 64])
 def test_evict_few_and_more(cuda_device, m):
     """Numbers around the one up to which pairs are picked one after the other, in
     rows longer than a block has threads, many heads to a cluster."""
