@@ -14,6 +14,11 @@ keys (L1) plus a d_k x d_v matrix A written only by pairs evicted from the
 window, A <- lambda A + eta k v^T, read as m = q A (L2), fused as
 y = y_local + sigmoid(g) m.  Within a step the eviction is written before the
 read.
+
+Around it: rotate and rotate_backward (rotary positions of q and k), and
+PagedCache with cache_append, cache_attend, cache_evict and cache_step, the
+streaming state for rows of different lengths and grouped heads, in which the
+least attended pair leaves into A instead of the oldest.
 """
 from __future__ import annotations
 
