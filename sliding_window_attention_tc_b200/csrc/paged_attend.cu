@@ -925,14 +925,19 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
             s_t[tid] = off - s_h[tid] * units;  // the last kExtra hold no pairs
         }
         __syncthreads();
-        // pool row and pairs of every run of 16
-        for (int x = tid; x < nt * (kTile / kRun); x += kJoinThreads) {
+        // pool row and pairs of every run of 16 (by the upper warps first: the lower
+        // ones have the first statistics to fetch), its weights asked into L2
+        for (int x = tid ^ (kJoinThreads / 2); x < nt * (kTile / kRun); x += kJoinThreads) {
             const int i = x / (kTile / kRun), b = s_b[i], j = s_t[i] * kTile + x % (kTile / kRun) * kRun;
             int nv = max(0, min(kRun, (int)row_pairs(p, b) - j)), row = 0;
             if (nv) {
                 const int pi = c.page_of(j), pg = c.table[(int64_t)b * c.max_pages + pi];
-                if (page_ok(c, pg)) row = (pg * c.H + s_h[i]) * c.page + j - pi * c.page;
-                else nv = 0;
+                if (page_ok(c, pg)) {
+                    row = (pg * c.H + s_h[i]) * c.page + j - pi * c.page;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(c.mass + row));
+                } else {
+                    nv = 0;
+                }
             }
             s_row[x] = row;
             s_nv[x] = nv;
