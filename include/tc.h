@@ -516,7 +516,10 @@ TC_API tc_status tc_cache_append(const tc_paged_cache *cache, const tc_rotary *r
  *   B Hq max_pages page < 2^38; g [Hq] float32, NULL exactly
  *   when cache->A is NULL or the memory is not to be read.
  * Work is split over the lengths and joined: two launches.  Every sum has a
- * fixed order on a given device.  Workspace:
+ * fixed order on a given device.  After TC_ERR_DEVICE_TIMEOUT in the status
+ * word y is not defined, and mass is as it was for every (row, key/value head)
+ * of which not all pairs were read (a step's pairs have entered and left).
+ * Workspace:
  * tc_cache_attend_workspace_size(cache, Hq, flags) bytes ((size_t)-1 when
  * invalid).  Errors as tc_prefill. */
 TC_API size_t tc_cache_attend_workspace_size(const tc_paged_cache *cache, int64_t Hq, uint32_t flags);

@@ -306,12 +306,8 @@ __global__ void __launch_bounds__(kBThreads + 32) attend_bf16_kernel(const __gri
         asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
         int st = 0;
         uint32_t round = 0;  // times the ring went around
-        bool dead = false;
         for (bool more = true; more;) {
-            if (round > 0 && !mbar_wait(&s_free[st], (round - 1) & 1u, &s_abort, p.c.status, p.wait_ns)) {
-                dead = true;
-                break;
-            }
+            if (round > 0 && !mbar_wait(&s_free[st], (round - 1) & 1u, &s_abort, p.c.status, p.wait_ns)) break;
             int n = max(0, min(box_rows, cur.n - j));
             if (n && !page_ok(p.c, page)) {
                 report(p.c.status, TC_ERR_DEVICE_BOUNDS);
@@ -346,12 +342,20 @@ __global__ void __launch_bounds__(kBThreads + 32) attend_bf16_kernel(const __gri
                 ++round;
             }
         }
-        // after a wait that ran out: no copy may land once the block is gone
-        if (dead)
-            for (int s = 0; s < S::STAGES; ++s) {
-                const uint32_t uses = round + (s < st ? 1 : 0);  // loads into stage s so far
-                if (uses) mbar_wait_drain(&s_full[s], (uses - 1) & 1u);
-            }
+        // No copy may land once the block is gone, and whether a computing warp gave
+        // up on one is not known here: the lanes stay until all have landed.  A lane
+        // whose wait ran out is at most one use of a stage behind the others (the
+        // next use waits for the computing warps, and they for this lane); it
+        // arrives for that one, so that the phase the others wait for ends.  The
+        // computing warps look at s_abort behind every wait and do not take the
+        // stage for a loaded one.
+        const uint32_t lanes = (1u << boxes) - 1u;
+        __syncwarp(lanes);
+        for (int s = 0; s < S::STAGES; ++s) {
+            const uint32_t uses = round + (s < st ? 1 : 0), most = __reduce_max_sync(lanes, uses);
+            if (uses < most) mbar_arrive(&s_full[s]);
+            if (most) mbar_wait_drain(&s_full[s], (most - 1) & 1u);
+        }
         return;
     }
 
@@ -395,9 +399,13 @@ __global__ void __launch_bounds__(kBThreads + 32) attend_bf16_kernel(const __gri
                 for (int e = 0; e < 4; ++e) o[t][k][e] = 0.f;
         }
         for (int i = 0; i < cur.count; ++i) {
-            if (!dead && !mbar_wait(&s_full[st], parity, &s_abort, p.c.status, p.wait_ns)) dead = true;
+            RunNote note{};
+            if (!dead) {
+                dead = !mbar_wait(&s_full[st], parity, &s_abort, p.c.status, p.wait_ns);
+                note = s_note[st][warp];
+                if (*const_cast<volatile int *>(&s_abort)) dead = true;  // a loading lane arrived without its rows
+            }
             if (dead) break;
-            const RunNote note = s_note[st][warp];
             if (note.pairs) {
                 const uint32_t base = ring + st * S::STAGE_BYTES;
                 // S^T = K Q^T, in two chains of products
@@ -566,7 +574,8 @@ __global__ void __launch_bounds__(kBThreads + 32) attend_bf16_kernel(const __gri
 #pragma unroll
             for (int w = 0; w < kBWarps; ++w) ls += s_l[w][tid] * ex2(s_m[w][tid] - (mx == -INFINITY ? 0.f : mx));
             part[S::HEADS * D + 2 * tid] = mx;
-            part[S::HEADS * D + 2 * tid + 1] = ls;
+            // after a wait that ran out the stretch may lack pairs: no sum is negative
+            part[S::HEADS * D + 2 * tid + 1] = *const_cast<volatile int *>(&s_abort) ? -1.f : ls;
         }
         warps_sync();
     }
@@ -729,7 +738,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
     constexpr int WU = kTile / 32;            // pairs per lane in flight (weights)
     __shared__ float s_q[HB][D];
     __shared__ __align__(16) float s_m[kMassStats], s_l[kMassStats];
-    __shared__ int s_b[kMassTiles], s_h[kMassTiles], s_t[kMassTiles];
+    __shared__ int s_b[kMassTiles], s_h[kMassTiles], s_t[kMassTiles], s_lost[kMassTiles];
     __shared__ int s_row[kMassTiles * (kTile / kRun)], s_nv[kMassTiles * (kTile / kRun)];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const CacheParams &c = p.c;
@@ -923,6 +932,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
             s_b[tid] = lo;
             s_h[tid] = off / units;
             s_t[tid] = off - s_h[tid] * units;  // the last kExtra hold no pairs
+            s_lost[tid] = 0;
         }
         __syncthreads();
         // pool row and pairs of every run of 16 (by the upper warps first: the lower
@@ -948,6 +958,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
             const int i = x < nt * p.G ? x / p.G : 0, g = x - i * p.G, b = s_b[i], h = s_h[i];
             const bool lead = x < nt * p.G && (i == 0 || s_t[i] == 0);
             float M = -INFINITY, L = 0.f;
+            bool lost = false;  // a stretch of the row that a wait cut short
             if (lead) {
                 const int units = pre[b + 1] - pre[b], tiles = units - kExtra, grp = g / p.heads, hh = g - grp * p.heads;
                 const uint32_t u0 = (uint32_t)pre[b] * per_row + (h * p.items + grp) * units;
@@ -956,6 +967,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
 #pragma unroll 4
                 for (int k = l8; k < np; k += 8) {
                     const float2 v = *reinterpret_cast<const float2 *>(ml + k * pf);
+                    lost |= v.y < 0.f;
                     const float mx = fmaxf(M, v.x), ref = mx == -INFINITY ? 0.f : mx;
                     L = fmaf(L, ex2(M - ref), v.y * ex2(v.x - ref));
                     M = mx;
@@ -968,6 +980,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
                 L = L * ex2(M - ref) + l2 * ex2(m2 - ref);
                 M = mx;
             }
+            if (lost) s_lost[i] = 1;
             if (lead && l8 == 0) {
                 s_m[x] = M == -INFINITY ? 0.f : M;
                 s_l[x] = L == 0.f ? 0.f : 1.f / L;
@@ -976,7 +989,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(const __gr
         __syncthreads();
         // a warp per tile, WU pairs a lane: the statistics are the warp's
         for (int i = warp; i < nt; i += kJoinThreads / 32) {
-            const int stat = (i - min(i, s_t[i])) * p.G;  // of the (row, head)'s first tile of the chunk
+            const int first = i - min(i, s_t[i]), stat = first * p.G;  // the (row, head)'s first tile of the chunk
+            if (s_lost[first]) continue;  // not all of its scores are there: its weights stay as they are
             int row[WU];
             float w[WU], old[WU];
 #pragma unroll
