@@ -469,7 +469,8 @@ typedef struct tc_paged_cache {
     void *k_pages, *v_pages;     /* [n_pages,H,page,d]                         */
     float *mass;                 /* [n_pages,H,page] accumulated weight; NULL when no
                                     call accumulates or evicts                 */
-    int32_t *pos;                /* [n_pages,H,page] position of the pair; NULL as mass */
+    int32_t *pos;                /* [n_pages,H,page] position of the pair, not negative (a
+                                    negative one is ordered by its low 31 bits); NULL as mass */
     const int32_t *table;        /* [B,max_pages]; entries past a row's pages are not read */
     int64_t *len;                /* [B] pairs held; negative: an empty row, which every
                                     call leaves untouched                      */

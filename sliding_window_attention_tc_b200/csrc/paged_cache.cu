@@ -169,7 +169,9 @@ cudaError_t launch_append_vec(const AppendParams &p, cudaStream_t s) {
 // ---- eviction -------------------------------------------------------------------
 
 // The order in which pairs leave, as one number: unprotected first, then by
-// weight (NaN last, -0 as 0), then by position.
+// weight (NaN last, -0 as 0), then by position.  No number is free to stand for
+// "no pair" (a protected NaN at position 2^31 - 1 has them all set), so pairs are
+// compared with their slots: no pair is (~0, ~0), behind every slot there is.
 __device__ __forceinline__ uint64_t leave_key(float mass, int32_t pos, int64_t protect_from) {
     uint32_t u = __float_as_uint(mass + 0.f);
     u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_
     if (m == 1) {
         const int64_t protect_from = clock0 + (STEP ? 1 : 0) - p.recent;
         uint64_t best = ~0ull;
-        uint32_t slot = 0xffffffffu;
+        uint32_t slot = tid < seen ? (uint32_t)tid : 0xffffffffu;  // its own pairs may all be the last there is
         for (int s0 = tid;;) {
 #pragma unroll
             for (int i = 0; i < kScanBatch; ++i) {
@@ -989,7 +991,7 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
                 slot = 0xffffffffu;
                 for (int s = tid, j = 0; s < n; s += kBulkThreads, ++j) {
                     const uint64_t key = (uint64_t)(place[s] >> 31) << 63 | (uint64_t)weight[s] << 31 | (place[s] & 0x7fffffffu);
-                    if (!(gone >> (j & 31) & 1u) && key < first) {
+                    if (!(gone >> (j & 31) & 1u) && less_pair(key, (uint32_t)s, first, slot)) {
                         first = key;
                         slot = (uint32_t)s;
                     }
