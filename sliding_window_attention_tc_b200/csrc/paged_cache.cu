@@ -21,6 +21,7 @@
 // cores) and stores the new lengths, which the first has to leave for its other
 // blocks to read.
 
+#include <atomic>
 #include <type_traits>
 
 #include "paged_cache.cuh"
@@ -1300,21 +1301,45 @@ cudaError_t launch_one(const EvictParams &p, int slices, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, evict_one_kernel<T, D, STEP>, p, slices);
 }
 
+// Shared memory of a bulk eviction of rows of up to n2 pairs.
+template <typename T, int D>
+constexpr size_t bulk_smem(int n2) {
+    const size_t sum = BulkShape<T, D>::SUM, sort = sort_room(n2);
+    return order_room(n2) + (sum > sort ? sum : sort);
+}
+
+// The kernel's leave to use that much is state of the process: it is granted for
+// the longest rows, and once per device, so that no call lowers what another
+// thread's is about to use.  Before a call's first kernel, so that a refusal leaves
+// the cache as it was.
 template <typename T, int D, int SL>
-cudaError_t launch_bulk(const EvictParams &p, cudaStream_t s) {
+cudaError_t grant_bulk() {
+    static std::atomic<uint64_t> granted{0};  // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (granted.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = allow_smem(evict_bulk_kernel<T, D, SL>, bulk_smem<T, D>(kSortMax));
+    if (e == cudaSuccess) granted.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+template <typename T, int D, int SL>
+cudaError_t launch_bulk(const EvictParams *launch, cudaStream_t s) {
+    if (!launch) return grant_bulk<T, D, SL>();
+    const EvictParams &p = *launch;
     const int64_t cap = pairs_room(p.c.capacity());
     const int n2 = (int)(cap < kSortMax ? cap : kSortMax);  // pairs sorted in shared memory
-    const size_t sum = BulkShape<T, D>::SUM, sort = sort_room(n2);
-    const size_t smem = order_room(n2) + (sum > sort ? sum : sort);
-    cudaError_t e = allow_smem(evict_bulk_kernel<T, D, SL>, smem);
-    if (e != cudaSuccess) return e;
+    const size_t smem = bulk_smem<T, D>(n2);
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = cluster_launch(attr, (int64_t)p.c.B * p.c.H * SL, kBulkThreads, smem, SL, true, s);
     return cudaLaunchKernelEx(&cfg, evict_bulk_kernel<T, D, SL>, p, n2);
 }
 
+// (p null: the grant alone)
 template <typename T, int D>
-cudaError_t launch_bulk_sl(const EvictParams &p, int slices, cudaStream_t s) {
+cudaError_t launch_bulk_sl(const EvictParams *p, int slices, cudaStream_t s) {
     if constexpr (D >= 64)
         if (slices == 4) return launch_bulk<T, D, 4>(p, s);
     if constexpr (D >= 32)
@@ -1323,7 +1348,7 @@ cudaError_t launch_bulk_sl(const EvictParams &p, int slices, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t launch_bulk_d(const EvictParams &p, int d, int slices, cudaStream_t s) {
+cudaError_t launch_bulk_d(const EvictParams *p, int d, int slices, cudaStream_t s) {
     switch (d) {
         case 16: return launch_bulk_sl<T, 16>(p, slices, s);
         case 32: return launch_bulk_sl<T, 32>(p, slices, s);
@@ -1392,9 +1417,13 @@ cudaError_t launch_cache_step_insert(const EvictParams &p, tc_dtype dtype, int d
 cudaError_t launch_cache_evict(const EvictParams &p, tc_dtype dtype, int d, int num_sms, cudaStream_t s) {
     const int64_t BH = (int64_t)p.c.B * p.c.H;
     const int one = evict_slices(BH, d, num_sms), bulk = bulk_slices(BH, d, num_sms);
-    const cudaError_t e = dtype == TC_BF16 ? launch_one_d<__nv_bfloat16, false>(p, d, one, s) : launch_one_d<float, false>(p, d, one, s);
+    auto bulk_call = [&](const EvictParams *launch) {
+        return dtype == TC_BF16 ? launch_bulk_d<__nv_bfloat16>(launch, d, bulk, s) : launch_bulk_d<float>(launch, d, bulk, s);
+    };
+    cudaError_t e = bulk_call(nullptr);
     if (e != cudaSuccess) return e;
-    return dtype == TC_BF16 ? launch_bulk_d<__nv_bfloat16>(p, d, bulk, s) : launch_bulk_d<float>(p, d, bulk, s);
+    e = dtype == TC_BF16 ? launch_one_d<__nv_bfloat16, false>(p, d, one, s) : launch_one_d<float, false>(p, d, one, s);
+    return e != cudaSuccess ? e : bulk_call(&p);
 }
 
 }  // namespace tc

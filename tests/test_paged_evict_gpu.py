@@ -36,3 +36,42 @@ def test_pairs_that_are_the_last_of_all(cuda_device, d, H, pos, m, whole):
     cpu.mass = cpu.mass.float().double()
     same_state(c, cpu, A_terms=n)
     assert tc.device_status() == 0
+
+
+def test_two_threads_whose_tables_differ(cuda_device):
+    """Evictions of two host threads at once, from caches whose tables are of
+    different sizes (and so ask for different shared memory): neither takes the
+    other's leave away."""
+    import threading
+
+    import sliding_window_attention_tc_b200 as tc
+    made = [make([90, 80], d=64, H=2, seed=1, room=0, width=128 * w) for w in (1, 8)]  # 2048 and 16384 slots a row
+    made.append(make([90, 80], d=64, H=2, seed=1, room=0, width=6))
+    errors, start = [], threading.Barrier(len(made))
+
+    def work(c, lens):
+        try:
+            s, ws = torch.cuda.Stream(), tc.cache_evict_workspace(c)
+            s.wait_stream(torch.cuda.default_stream())
+            start.wait()
+            with torch.cuda.stream(s):
+                for _ in range(3000):
+                    c.lens.copy_(lens)
+                    tc.cache_evict(c, 60, workspace=ws)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    lens = [c.lens.clone() for c, _ in made]
+    for c, cpu in made:  # the first eviction, checked by itself
+        tc.cache_evict(c, 60)
+        cpu.evict(60, 1)
+        same_state(c, cpu, A_terms=40)
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(c, n)) for (c, _), n in zip(made, lens)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert all(c.lens.tolist() == [60, 60] for c, _ in made) and tc.device_status() == 0
