@@ -760,10 +760,12 @@ def _addr(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.data_ptr()
 
 
-def _raw_stream(dev: int, *ts, stream=None, used=()):
+def _raw_stream(dev: int, *ts, stream=None, used=(), made=False):
     """The stream to launch on, for tensors that must all be on CUDA device
     `dev`, the current one.  `used`: what the call may have allocated itself,
-    on the current stream; the allocator learns that a given stream uses it."""
+    on the current stream; the allocator learns that a given stream uses it.
+    `made`: it did allocate: the memory may be a block that work queued on the
+    current stream still writes, so a given stream waits for that work first."""
     for t in ts:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensor on {t.device}; the call's other tensors are on "
@@ -775,6 +777,8 @@ def _raw_stream(dev: int, *ts, stream=None, used=()):
                          "call under torch.cuda.device(...) of the tensors' device")
     if stream is None:
         return _current_stream(dev)
+    if made and stream.cuda_stream != _current_stream(dev):
+        stream.wait_stream(torch.cuda.current_stream(dev))
     for t in used:
         if t is not None:
             t.record_stream(stream)
@@ -796,6 +800,7 @@ def _rotate(q, k, rotary, positions, t0, q_out, k_out, flags, stream):
     if len(qn) != 4:
         raise ValueError("q must be [B,Hq,T,d]")
     B, Hq, T, d = qn
+    made = q_out is None or (k is not None and k_out is None)
     if q_out is None:
         q_out = torch.empty(qn, dtype=dtype, device=q.device)
     a, c = _rows(q, "q", qn, dtype), _rows(q_out, "q_out", qn, dtype)
@@ -819,7 +824,7 @@ def _rotate(q, k, rotary, positions, t0, q_out, k_out, flags, stream):
         pp = positions.data_ptr()
     desc = _PACK_ROTATE.pack(B, Hq, H, T, d, _dtype_code(q), flags, a[0], a[1], a[2], b[0], b[1], b[2], c[0], c[1], c[2],
                              e[0], e[1], e[2])
-    s = _raw_stream(q.get_device(), k, q_out, k_out, positions, stream=stream, used=(q_out, k_out))
+    s = _raw_stream(q.get_device(), k, q_out, k_out, positions, stream=stream, used=(q_out, k_out), made=made)
     st = _lib.tc_rotate(desc, rotary.ref, pp, t0, q.data_ptr(), kp, q_out.data_ptr(), kop, s)
     if st:
         raise TCError(st, "tc_rotate")
@@ -944,6 +949,7 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, rotary:
     kn = (B, H, T, d)
     ks, vs = _rows(k, "k", kn, cache.dtype), _rows(v, "v", kn, cache.dtype)
     qs, Hq = _NO_STRIDE, 0
+    made = q is not None and q_out is None
     if q is not None:
         if q.dim() != 4:
             raise ValueError("q must be [B,Hq,T,d]")
@@ -961,7 +967,7 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, rotary:
     if mass is not None:
         _expect(mass, "mass", (B, H, T), torch.float32)
     _contig(counts, mass, q_out)
-    s = _raw_stream(cache.dev, k, v, q, q_out, counts, mass, stream=stream, used=(q_out,))
+    s = _raw_stream(cache.dev, k, v, q, q_out, counts, mass, stream=stream, used=(q_out,), made=made)
     a = _PACK_APPEND.pack(T, Hq, _addr(q), k.data_ptr(), v.data_ptr(), *qs[:3], *ks[:3], *vs[:3], _addr(counts),
                           _addr(mass), _addr(q_out))
     st = _lib.tc_cache_append(cache.ref, None if rotary is None else rotary.ref, a, s)
@@ -990,6 +996,7 @@ def cache_attend(cache: PagedCache, q: torch.Tensor, *, g: Optional[torch.Tensor
             raise ValueError("g reads the memory, but the cache has none")
     if accumulate and cache.mass is None:
         raise ValueError("accumulate needs a cache with mass")
+    made = y is None or workspace is None
     if y is None:
         y = torch.empty_like(q)
     elif y.shape != q.shape or y.dtype is not cache.dtype:
@@ -998,7 +1005,7 @@ def cache_attend(cache: PagedCache, q: torch.Tensor, *, g: Optional[torch.Tensor
     n = 0 if workspace is not None else _lib.tc_cache_attend_workspace_size(cache.ref, Hq, flags)
     workspace, room = _workspace(n, "tc_cache_attend_workspace_size", workspace, cache.device)
     _contig(q, g, y)
-    s = _raw_stream(cache.dev, q, g, y, workspace, stream=stream, used=(y, workspace))
+    s = _raw_stream(cache.dev, q, g, y, workspace, stream=stream, used=(y, workspace), made=made)
     st = _lib.tc_cache_attend(cache.ref, Hq, q.data_ptr(), _addr(g), y.data_ptr(), flags, workspace.data_ptr(), room, s)
     if st:
         raise TCError(st, "tc_cache_attend")
@@ -1027,9 +1034,10 @@ def cache_evict(cache: PagedCache, budget: int, *, recent: int = 1,
     pairs of the last `recent` positions go last."""
     if cache.mass is None:
         raise ValueError("eviction needs a cache with mass and pos")
-    n = 0 if workspace is not None else _lib.tc_cache_evict_workspace_size(cache.ref)
+    made = workspace is None
+    n = _lib.tc_cache_evict_workspace_size(cache.ref) if made else 0
     workspace, room = _workspace(n, "tc_cache_evict_workspace_size", workspace, cache.device)
-    s = _raw_stream(cache.dev, workspace, stream=stream, used=(workspace,))
+    s = _raw_stream(cache.dev, workspace, stream=stream, used=(workspace,), made=made)
     _check(_lib.tc_cache_evict(cache.ref, int(budget), int(recent), workspace.data_ptr(), room, s), "tc_cache_evict")
 
 
@@ -1057,6 +1065,7 @@ def cache_step(cache: PagedCache, q: torch.Tensor, k: torch.Tensor, v: torch.Ten
             raise ValueError("g reads the memory, but the cache has none")
     if cache.mass is None:
         raise ValueError("a step needs a cache with mass and pos")
+    made = y is None or workspace is None
     if y is None:
         y = torch.empty((cache.B, Hq, cache.d), dtype=cache.dtype, device=q.device)
     elif y.shape != q.shape or y.dtype is not cache.dtype:
@@ -1065,7 +1074,7 @@ def cache_step(cache: PagedCache, q: torch.Tensor, k: torch.Tensor, v: torch.Ten
     n = 0 if workspace is not None else _lib.tc_cache_step_workspace_size(cache.ref, Hq, flags)
     workspace, room = _workspace(n, "tc_cache_step_workspace_size", workspace, cache.device)
     _contig(g, y)
-    s = _raw_stream(cache.dev, q, k, v, g, y, workspace, stream=stream, used=(y, workspace))
+    s = _raw_stream(cache.dev, q, k, v, g, y, workspace, stream=stream, used=(y, workspace), made=made)
     a = _PACK_STEP.pack(Hq, q.data_ptr(), k.data_ptr(), v.data_ptr(), *qs[:2], *ks[:2], *vs[:2], _addr(g), y.data_ptr(),
                         int(budget), int(recent), flags)
     st = _lib.tc_cache_step(cache.ref, None if rotary is None else rotary.ref, a, workspace.data_ptr(), room, s)
