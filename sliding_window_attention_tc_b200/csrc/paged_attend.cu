@@ -473,14 +473,19 @@ __global__ void __launch_bounds__(kBThreads + 32) attend_bf16_kernel(const __gri
                         z[e + 2] = ex2(z[e + 2] - ref);
                         l[t][e] = fmaf(l[t][e], corr[t][e], z[e] + z[e + 2]);
                     }
-                    // P^T as a bf16 pair: hi rounded, lo the rest
+                    // P^T as a bf16 pair: hi cut off, lo the rest, so that both have the
+                    // weight's sign.  A weight above zero has no lo of zero (the least
+                    // bf16 instead, 2^-126): an infinite value then stays infinite in
+                    // both products, where 0 * inf would make it NaN.
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
+                        constexpr float least = 1.17549435e-38f;
                         const float x = z[2 * e], y = z[2 * e + 1];
-                        const uint32_t hi = pack_bf16(x, y);
-                        const uint32_t lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
-                        ph[t][e] = transpose8x8(hi);
-                        pl[t][e] = transpose8x8(lo);
+                        const uint32_t hx = __float_as_uint(x) & 0xffff0000u, hy = __float_as_uint(y) & 0xffff0000u;
+                        const float lx = fmaxf(x - __uint_as_float(hx), fminf(x, least));
+                        const float ly = fmaxf(y - __uint_as_float(hy), fminf(y, least));
+                        ph[t][e] = transpose8x8(__byte_perm(hx, hy, 0x7632));
+                        pl[t][e] = transpose8x8(pack_bf16(lx, ly));
                     }
                 }
                 if (__any_sync(0xffffffffu, grew)) {
