@@ -845,6 +845,23 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t (&o)[3]) {
     }
 }
 
+// The same sum for four neighbours of one row of A, pair after pair in float32: for
+// what is not finite.  It ends once all four are NaN, which no pair changes.
+template <typename T, int D>
+__device__ __noinline__ float4 sum_of_products(const T *kp, const T *vp, const uint32_t *order, const float *factor, int m, int r, int col) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < m; ++i) {
+        const T *v = vp + (int64_t)order[i] * D + col;
+        const float wk = factor[i] * to_f32(kp[(int64_t)order[i] * D + r]);
+        a.x = fmaf(wk, to_f32(v[0]), a.x);
+        a.y = fmaf(wk, to_f32(v[1]), a.y);
+        a.z = fmaf(wk, to_f32(v[2]), a.z);
+        a.w = fmaf(wk, to_f32(v[3]), a.w);
+        if (a.x != a.x && a.y != a.y && a.z != a.z && a.w != a.w) break;
+    }
+    return a;
+}
+
 // Shared memory of one block: the order of the pairs, then, one after the
 // other in the same room, what sorting needs (keys, positions, a second order,
 // counts), what the sum needs (raw tiles, parts; its result), and the lists of
@@ -1200,6 +1217,11 @@ __global__ void __launch_bounds__(kBulkThreads, D <= 64 ? 2 : 1) evict_bulk_kern
                 add.z += y.z;
                 add.w += y.w;
             }
+            // a key's or value's second and third parts may be 0, and 0 * inf is NaN
+            // where the pair's own product is infinite: what came out as NaN is summed
+            // again from whole values
+            if (add.x != add.x || add.y != add.y || add.z != add.z || add.w != add.w)
+                add = sum_of_products<T, D>(kp, vp, order, factor, m, at / (D / 4), at % (D / 4) * 4);
             float4 *dst = reinterpret_cast<float4 *>(c.A + bh * D * D) + at;
             float4 o = *dst;
             o.x = fmaf(lm, o.x, eta * add.x);

@@ -43,3 +43,38 @@ def test_attend(cuda_device, dtype, d, H, G, page):
         tol = tol + torch.finfo(DT[dtype]).eps / 2 * (want.abs() + tol)
         same(tc.cache_attend(c, q.cuda(), g=None if gate is None else gate.cuda()), want, tol)
     assert tc.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,H,rows", [(64, 2, 3), (128, 1, 3), (16, 2, 3), (64, 8, 40), (128, 4, 30)])
+@pytest.mark.parametrize("m", [1, 2, 12, 300])
+def test_evict(cuda_device, dtype, d, H, rows, m):
+    """Pairs that leave with infinite keys, values or both; of both signs (NaN),
+    against a zero (NaN), a NaN; ones that fit bf16."""
+    import sliding_window_attention_tc_b200 as tc
+    budget = 30
+    c, cpu = make([budget + m] * rows, d=d, H=H, dtype=dtype, seed=m + d, room=0)
+    for b in range(rows):
+        slots = range(budget + m)
+        pg, sl = cpu.at(b, slots)
+        put = lambda x, y, i, col, val: [t.__setitem__((pg[i].to(t.device), slice(None), sl[i].to(t.device), col), val) for t in (x, y)]  # noqa: E731
+        for x in (c.mass, cpu.mass):  # the first m slots leave, in their order
+            x[pg.to(x.device), :, sl.to(x.device)] = torch.arange(budget + m)[:, None].to(x)
+        kk, vv = (c.k_pages, cpu.k), (c.v_pages, cpu.v)
+        for i in range(0, m, 5):  # values that fit bf16's first part, so that a float32's other parts are 0
+            put(*vv, i, slice(8, 12), 0.5)
+        put(*vv, 0, 0, math.inf)
+        put(*vv, m - 1, 1, -math.inf)
+        if b % 3 == 1:
+            put(*kk, m // 2, 2, math.inf)
+            put(*vv, m // 2, 4, -math.inf)
+            put(*vv, m // 2, 5, 0.0)  # inf * 0
+        if b % 3 == 2 and m > 1:
+            put(*vv, m - 1, 0, -math.inf)
+            put(*vv, m // 2, 3, math.nan)
+    tc.cache_evict(c, budget, recent=1)
+    cpu.evict(budget, 1)
+    assert c.lens.tolist() == cpu.lens and torch.equal(c.pos.cpu().long(), cpu.pos)
+    assert torch.isinf(cpu.A).any() and torch.isfinite(cpu.A).any()
+    same(c.A, cpu.A, (m + 32) * 2.0 ** -23 * cpu.A_abs)
+    assert tc.device_status() == 0
