@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kOneThreads, 4) evict_one_kernel(const __grid_
         const int cg = tid % CG, rg = tid / CG;
         const float lam = c.lam[h], eta = c.eta[h];
         const float4 v4 = m == 1 ? reinterpret_cast<const float4 *>(s_v)[cg] : make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int g0 = 0; g0 == 0 || g0 < G; g0 += kQBatch) {
+        for (int g0 = 0; g0 == 0 || (read && g0 < G); g0 += kQBatch) {
             const int ng = read ? min(kQBatch, G - g0) : 0;
             if (g0 > 0) {  // (read) later batches: the queries again
                 for (int x = tid; x < ng * D; x += kOneThreads) {
