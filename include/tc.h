@@ -406,7 +406,7 @@ typedef struct tc_rotary {
     double factor;     /* >= 1                                                 */
     double low, high;  /* turns over train_len; high <= low: no ramp           */
     double train_len;  /* >= 0, used by the ramp only                          */
-    double gain;       /* finite; multiplies the rotated part                  */
+    double gain;       /* finite as a float32; multiplies the rotated part     */
 } tc_rotary;
 
 #define TC_ROTATE_BACKWARD 1u /* the transposed rotation: gradients of the inputs

@@ -86,7 +86,7 @@ bool make_rotary_table(const tc_rotary *r, int64_t d, RotaryTable *out) {
     if (r->rot < 0 || r->rot > d || r->rot % 2 || (r->interleaved != 0 && r->interleaved != 1)) return false;
     if (!(r->base > 1.0) || !(r->factor >= 1.0) || !(r->train_len >= 0.0)) return false;
     if (!std::isfinite(r->base) || !std::isfinite(r->factor) || !std::isfinite(r->train_len) ||
-        !std::isfinite(r->gain) || !std::isfinite(r->low) || !std::isfinite(r->high))
+        !std::isfinite((float)r->gain) || !std::isfinite(r->low) || !std::isfinite(r->high))
         return false;
     out->rot = (int)r->rot;
     out->interleaved = (int)r->interleaved;
