@@ -21,12 +21,12 @@
 // O^T = V^T P^T with m16n8k16: with the pairs as M, eight heads fill a product
 // that would be half empty with the heads as M, and the same lanes hold a
 // head's scores and its outputs, so rescaling needs no exchange.  P enters as a
-// bf16 pair hi + lo, so the outputs keep float32's precision up to their one
-// rounding.  The tensor pipe is nowhere near busy (16 d multiply-adds a pair
-// against 4 d bytes); a warp's chain score -> maximum -> weight -> output is
-// what has to be hidden, by the other warps and the loads in flight.  (Four
-// warps of 32 pairs each took 2090 cycles a tile with the data at hand, where
-// memory brings one in 2670.)
+// bf16 pair hi + lo (off by 2^-17 of a weight; a bf16 result is rounded by 2^-8).
+// The tensor pipe is nowhere near busy (16 d multiply-adds a pair against 4 d
+// bytes); a warp's chain score -> maximum -> weight -> output is what has to be
+// hidden, by the other warps and the loads in flight.  (Four warps of 32 pairs
+// each took 2090 cycles a tile with the data at hand, where memory brings one in
+// 2670.)
 //
 // float32: the same walk with float32 multiply-adds, d/4 lanes per pair.
 

@@ -20,8 +20,13 @@ struct RotaryTable {
 // cos and sin (times gain) of position p at frequency inc.  The nearest
 // quarter turn is taken off in integers; the rest, at most an eighth of a turn,
 // is exact to 2^-32 turns.  There the Taylor series of sin and cos need five and
-// six terms: the next ones are below 2^-29 at pi/4.  (CUDA's sincospif, which
-// reduces its argument again, made the LM shape's rotation a fifth slower.)
+// six terms: the next ones are below 2^-29 at pi/4.  t is off by three roundings,
+// 3 2^-24 t, which makes 2^-23.2 of a sine or cosine at most; with the sums' own
+// roundings (2^-25 for the last, 2^-26 for the others) and the remainder both are
+// off by less than 2^-22.  A rotated element adds gain, its product with cos or
+// sin, a product and a sum, 2^-24 each: 2^-21 of gain (|x| + |z|) in all.  (CUDA's
+// sincospif, which reduces its argument again, made the LM shape's rotation a
+// fifth slower.)
 __device__ __forceinline__ void rotary_angle(int64_t p, uint64_t inc, float gain, float &c, float &s) {
     const uint32_t u = (uint32_t)(((uint64_t)p * inc) >> 32);
     const uint32_t quarter = (u + 0x20000000u) >> 30;
